@@ -200,3 +200,131 @@ MX_API mx_status gemm_a8w8_ptpc_bf16(const void* qa, const float* sa, const void
     return launched(mx::launch_gemm_a8w8(qa, sa, qw, sw, y_bf16, M, N, K, workspace,
                                          reinterpret_cast<hipStream_t>(stream)));
 }
+
+MX_API mx_status b128_quant_act_fp8(const void* x_bf16, int64_t M, int64_t K, void* q, float* s, void* stream) {
+    mx_status st = check_rows(M, K, 128);
+    if (st != MX_SUCCESS) return st;
+    if (M == 0) return MX_SUCCESS;
+    if (!x_bf16 || !q || !s) return MX_ERROR_INVALID_VALUE;
+    if (!aligned(x_bf16, 16) || !aligned(q, 8) || !aligned(s, 4)) return MX_ERROR_MISALIGNED;
+    if ((st = check_device()) != MX_SUCCESS) return st;
+    return launched(mx::launch_quant_b128_act(x_bf16, M, K, q, s, reinterpret_cast<hipStream_t>(stream)));
+}
+
+MX_API mx_status b128_quant_weight_f32(const float* w, int64_t N, int64_t K, void* q, float* s, void* stream) {
+    mx_status st = check_rows(N, K, 128);
+    if (st != MX_SUCCESS) return st;
+    if ((N + 127) / 128 > INT32_MAX / (K / 128)) return MX_ERROR_UNSUPPORTED_SHAPE;  // one workgroup per block
+    if (N == 0) return MX_SUCCESS;
+    if (!w || !q || !s) return MX_ERROR_INVALID_VALUE;
+    if (!aligned(w, 16) || !aligned(q, 4) || !aligned(s, 4)) return MX_ERROR_MISALIGNED;
+    if ((st = check_device()) != MX_SUCCESS) return st;
+    return launched(mx::launch_quant_b128_weight(w, N, K, q, s, reinterpret_cast<hipStream_t>(stream)));
+}
+
+MX_API mx_status gemm_a8w8_b128_bf16(const void* qa, const float* sa, const void* qw, const float* sw, void* y_bf16,
+                                     int64_t M, int64_t N, int64_t K, void* stream) {
+    mx_status st = check_gemm(M, N, K);
+    if (st != MX_SUCCESS) return st;
+    if (M == 0 || N == 0) return MX_SUCCESS;
+    if (!qa || !sa || !qw || !sw || !y_bf16) return MX_ERROR_INVALID_VALUE;
+    if (!aligned(qa, 16) || !aligned(qw, 16) || !aligned(sa, 4) || !aligned(sw, 4) || !aligned(y_bf16, 2))
+        return MX_ERROR_MISALIGNED;
+    if ((st = check_device()) != MX_SUCCESS) return st;
+    return launched(mx::launch_gemm_b128(qa, sa, qw, sw, y_bf16, M, N, K, reinterpret_cast<hipStream_t>(stream)));
+}
+
+MX_API mx_status gemm_a8w8_b128_grouped_bf16(const void* qa, const float* sa, int64_t a_rows, const void* qw,
+                                             const float* sw, void* y_bf16, const int32_t* offsets, const int32_t* rows,
+                                             int64_t G, int64_t T, int64_t N, int64_t K, void* stream) {
+    mx_status st = check_gemm(T, N, K);
+    if (st != MX_SUCCESS) return st;
+    if (G < 0 || a_rows < 0) return MX_ERROR_INVALID_VALUE;
+    if (G > 65535 || a_rows > (INT64_C(1) << 40) / K || N > (INT64_C(1) << 40) / K / (G > 0 ? G : 1))
+        return MX_ERROR_UNSUPPORTED_SHAPE;
+    // 128-row tiles, one partial tile per group, must fit one 1-D grid
+    if ((T / 128 + (G < T ? G : T)) * ((N + 127) / 128) > INT32_MAX) return MX_ERROR_UNSUPPORTED_SHAPE;
+    if (G == 0 || T == 0 || N == 0) return MX_SUCCESS;
+    if (!qa || !sa || !qw || !sw || !y_bf16 || !offsets) return MX_ERROR_INVALID_VALUE;
+    if (a_rows == 0 || (!rows && a_rows < T)) return MX_ERROR_INVALID_VALUE;
+    if (!aligned(qa, 16) || !aligned(qw, 16) || !aligned(sa, 4) || !aligned(sw, 4) || !aligned(y_bf16, 2) ||
+        !aligned(offsets, 4) || !aligned(rows, 4))
+        return MX_ERROR_MISALIGNED;
+    if ((st = check_device()) != MX_SUCCESS) return st;
+    return launched(mx::launch_gemm_b128_grouped(qa, sa, a_rows, qw, sw, y_bf16, offsets, rows, G, T, N, K,
+                                                 reinterpret_cast<hipStream_t>(stream)));
+}
+
+// T >= 0 rows of 1 .. 1024 experts
+static mx_status check_router(int64_t T, int64_t E) {
+    if (T < 0) return MX_ERROR_INVALID_VALUE;
+    if (E < 1 || E > 1024 || T > INT32_MAX) return MX_ERROR_UNSUPPORTED_SHAPE;
+    return MX_SUCCESS;
+}
+
+static mx_status check_route(int64_t T, int64_t top, int64_t E) {
+    const mx_status st = check_router(T, E);
+    if (st != MX_SUCCESS) return st;
+    if (top < 0) return MX_ERROR_INVALID_VALUE;
+    // choices are numbered in 31 bits, and the place pass reads every chunk's counts in every workgroup
+    if (top > 0 && T > (INT64_C(1) << 24) / top) return MX_ERROR_UNSUPPORTED_SHAPE;
+    return MX_SUCCESS;
+}
+
+MX_API size_t moe_route_workspace_bytes(int64_t T, int64_t top, int64_t E) {
+    return check_route(T, top, E) == MX_SUCCESS ? mx::moe_route_workspace_bytes(T * top, E) : 0;
+}
+
+MX_API mx_status moe_route(const void* ids, int id_bytes, int64_t T, int64_t top, int64_t E, int32_t* counts,
+                           int32_t* offsets, int32_t* rows, int32_t* slots, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    mx_status st = check_route(T, top, E);
+    if (st != MX_SUCCESS) return st;
+    if (id_bytes != 4 && id_bytes != 8) return MX_ERROR_INVALID_VALUE;
+    const bool any = T * top > 0;
+    if (!counts || !offsets || (any && (!ids || !rows || !slots))) return MX_ERROR_INVALID_VALUE;
+    const size_t need = mx::moe_route_workspace_bytes(T * top, E);
+    if (workspace_bytes < need || (need && !workspace)) return MX_ERROR_WORKSPACE;
+    if (!aligned(ids, id_bytes) || !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4) ||
+        (need && !aligned(workspace, 16)))
+        return MX_ERROR_MISALIGNED;
+    if ((st = check_device()) != MX_SUCCESS) return st;
+    return launched(mx::launch_moe_route(ids, id_bytes == 8, T, top, E, counts, offsets, rows, slots, workspace,
+                                         reinterpret_cast<hipStream_t>(stream)));
+}
+
+MX_API size_t moe_balance_loss_workspace_bytes(int64_t T, int64_t E) {
+    return check_router(T, E) == MX_SUCCESS ? mx::moe_balance_workspace_bytes(T, E) : 0;
+}
+
+MX_API mx_status moe_balance_loss(const void* logits, mx_dtype dtype, int64_t T, int64_t E, const int32_t* counts,
+                                  const uint8_t* mask, float coef, float* loss, float* weights, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    mx_status st = check_router(T, E);
+    if (st != MX_SUCCESS) return st;
+    if (dtype != MX_F32 && dtype != MX_BF16) return MX_ERROR_INVALID_VALUE;
+    if (!counts || !loss || !weights || (T > 0 && !logits)) return MX_ERROR_INVALID_VALUE;
+    const size_t need = mx::moe_balance_workspace_bytes(T, E);
+    if (workspace_bytes < need || (need && !workspace)) return MX_ERROR_WORKSPACE;
+    if (!aligned(logits, dtype == MX_F32 ? 4 : 2) || !aligned(counts, 4) || !aligned(loss, 4) || !aligned(weights, 4) ||
+        (need && !aligned(workspace, 16)))
+        return MX_ERROR_MISALIGNED;
+    if ((st = check_device()) != MX_SUCCESS) return st;
+    return launched(mx::launch_moe_balance(logits, dtype == MX_BF16, T, E, counts, mask, coef, loss, weights, workspace,
+                                           reinterpret_cast<hipStream_t>(stream)));
+}
+
+MX_API mx_status moe_balance_loss_grad(const void* logits, mx_dtype dtype, int64_t T, int64_t E, const float* weights,
+                                       const uint8_t* mask, const float* grad_loss, void* dlogits, void* stream) {
+    mx_status st = check_router(T, E);
+    if (st != MX_SUCCESS) return st;
+    if (dtype != MX_F32 && dtype != MX_BF16) return MX_ERROR_INVALID_VALUE;
+    if (T == 0) return MX_SUCCESS;
+    if (!logits || !weights || !grad_loss || !dlogits) return MX_ERROR_INVALID_VALUE;
+    const uintptr_t size = dtype == MX_F32 ? 4 : 2;
+    if (!aligned(logits, size) || !aligned(dlogits, size) || !aligned(weights, 4) || !aligned(grad_loss, 4))
+        return MX_ERROR_MISALIGNED;
+    if ((st = check_device()) != MX_SUCCESS) return st;
+    return launched(mx::launch_moe_balance_grad(logits, dtype == MX_BF16, T, E, weights, mask, grad_loss, dlogits,
+                                                reinterpret_cast<hipStream_t>(stream)));
+}

@@ -36,6 +36,25 @@ hipError_t launch_gemm_a8w8(const void* qa, const float* sa, const void* qw, con
                             int64_t M, int64_t N, int64_t K, void* workspace, hipStream_t st);
 size_t gemm_a8w8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+// Block-128 FP8 (one FP32 scale per 128 values; K % 128 == 0): quantizers and GEMMs.
+hipError_t launch_quant_b128_act(const void* x, int64_t M, int64_t K, void* q, float* s, hipStream_t st);
+hipError_t launch_quant_b128_weight(const float* w, int64_t N, int64_t K, void* q, float* s, hipStream_t st);
+hipError_t launch_gemm_b128(const void* qa, const float* sa, const void* qw, const float* sw, void* y, int64_t M, int64_t N,
+                            int64_t K, hipStream_t st);
+hipError_t launch_gemm_b128_grouped(const void* qa, const float* sa, int64_t arows, const void* qw, const float* sw,
+                                    void* y, const int32_t* offsets, const int32_t* rows, int64_t G, int64_t M, int64_t N,
+                                    int64_t K, hipStream_t st);
+
+// Expert routing: packing of the experts' rows, and the balance loss with its gradient.
+size_t moe_route_workspace_bytes(int64_t n, int64_t E);
+hipError_t launch_moe_route(const void* ids, bool wide, int64_t T, int64_t top, int64_t E, int32_t* counts, int32_t* offsets,
+                            int32_t* rows, int32_t* slots, void* workspace, hipStream_t st);
+size_t moe_balance_workspace_bytes(int64_t T, int64_t E);
+hipError_t launch_moe_balance(const void* logits, bool half, int64_t T, int64_t E, const int32_t* counts, const uint8_t* mask,
+                              float coef, float* loss, float* w, void* workspace, hipStream_t st);
+hipError_t launch_moe_balance_grad(const void* logits, bool half, int64_t T, int64_t E, const float* w, const uint8_t* mask,
+                                   const float* grad_loss, void* dlogits, hipStream_t st);
+
 // Compute units of the current device (cached per device); 0 if the query fails.
 int device_cus();
 

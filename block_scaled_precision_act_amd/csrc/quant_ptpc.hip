@@ -27,34 +27,14 @@
 // both signs, subnormals included, found no difference.  Quotients here never
 // exceed 448 * (1 + 2^-23) < 464 (|x| <= a and s = fl32(a / 448)), so its
 // behaviour past the largest finite code never matters.
+#include "fp8_device.hpp"
 #include "launch.hpp"
-#include "mx_device.hpp"
 
 namespace mx {
 namespace {
 
 constexpr int kThreads = 512;
 constexpr int kVec = 2;  // 8-value vectors per thread kept in registers
-
-// fl32(x / s) for BF16 rows: r = fl32(1 / s) once per row, then the quotient q0 = fl32(x r) is
-// corrected twice with the remainder x - q s (exact, an FMA) scaled by r (Markstein's method); the
-// sign of x is restored for zeros.  Used only when s >= 2^-90, so that every remainder that can
-// decide a code is a normal number.  An exhaustive comparison with the IEEE division, over every
-// finite positive BF16 row maximum a (s = fl32(a / 448) >= 2^-90) and every BF16 x with |x| <= a,
-// found the same quotient wherever it is at least 2^-10 (below that every code is a signed zero)
-// and the same E4M3 code everywhere.
-__device__ __forceinline__ float div_corrected(float x, float s, float r) {
-    const float q0 = x * r;
-    const float q1 = __builtin_fmaf(__builtin_fmaf(-q0, s, x), r, q0);
-    const float q2 = __builtin_fmaf(__builtin_fmaf(-q1, s, x), r, q1);
-    return __builtin_copysignf(q2, x);
-}
-
-// E4M3fn codes of four binary32 quotients (|r| < 464), round to nearest even, packed low to high.
-__device__ __forceinline__ uint32_t e4m3fn_x4(float r0, float r1, float r2, float r3) {
-    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(r0, r1, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r2, r3, lo, true);
-}
 
 template <bool F32>
 struct Row8 {  // eight consecutive values of a row as binary32
@@ -93,18 +73,6 @@ struct Row8 {  // eight consecutive values of a row as binary32
         return make_uint2(e4m3fn_x4(q[0], q[1], q[2], q[3]), e4m3fn_x4(q[4], q[5], q[6], q[7]));
     }
 };
-
-// Maximum of v over the wave: DPP lane swaps within each row of 16 lanes (quad swaps, then the half-row
-// and row mirrors), then the four row maxima by readlane.  No LDS round trip; every lane must be active.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));  // row_half_mirror
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));  // row_mirror
-    const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0), b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
-    const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32), d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
-    return max(max(a, b), max(c, d));
-}
 
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void quant_ptpc_kernel(const void* __restrict__ x, uint8_t* __restrict__ q,

@@ -28,6 +28,7 @@ MX_ERROR_MISALIGNED = 3
 MX_ERROR_WORKSPACE = 4
 MX_ERROR_LAUNCH = 5
 MX_ERROR_DEVICE = 6
+MX_F32, MX_BF16 = 0, 1  # mx_dtype
 
 _lib = None
 
@@ -73,6 +74,21 @@ def lib() -> ctypes.CDLL:
         L.mx_linear_a4w4_bf16.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, ctypes.c_size_t, vp]
         L.mx_linear_a4w4_bf16.restype = i32
         L.mx_gemm_a4w4_grouped_bf16.restype = i32
+        sz, f32 = ctypes.c_size_t, ctypes.c_float
+        for name, args in (
+                ("b128_quant_act_fp8", [vp, i64, i64, vp, vp, vp]),
+                ("b128_quant_weight_f32", [vp, i64, i64, vp, vp, vp]),
+                ("gemm_a8w8_b128_bf16", [vp, vp, vp, vp, vp, i64, i64, i64, vp]),
+                ("gemm_a8w8_b128_grouped_bf16", [vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp]),
+                ("moe_route", [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, sz, vp]),
+                ("moe_balance_loss", [vp, i32, i64, i64, vp, vp, f32, vp, vp, vp, sz, vp]),
+                ("moe_balance_loss_grad", [vp, i32, i64, i64, vp, vp, vp, vp, vp])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = i32
+        L.moe_route_workspace_bytes.argtypes = [i64, i64, i64]
+        L.moe_route_workspace_bytes.restype = sz
+        L.moe_balance_loss_workspace_bytes.argtypes = [i64, i64]
+        L.moe_balance_loss_workspace_bytes.restype = sz
         _lib = L
     return _lib
 
@@ -132,6 +148,22 @@ def gemm_a8w8_ptpc_workspace_bytes(M, N, K) -> int:
 
 def gemm_a8w8_ptpc_bf16(qa, sa, qw, sw, y, M, N, K, workspace=None, workspace_bytes=0, stream=None) -> int:
     return lib().gemm_a8w8_ptpc_bf16(qa, sa, qw, sw, y, M, N, K, workspace, workspace_bytes, stream)
+
+
+def b128_quant_act_fp8(x, M, K, q, s, stream=None) -> int:
+    return lib().b128_quant_act_fp8(x, M, K, q, s, stream)
+
+
+def b128_quant_weight_f32(w, N, K, q, s, stream=None) -> int:
+    return lib().b128_quant_weight_f32(w, N, K, q, s, stream)
+
+
+def gemm_a8w8_b128_bf16(qa, sa, qw, sw, y, M, N, K, stream=None) -> int:
+    return lib().gemm_a8w8_b128_bf16(qa, sa, qw, sw, y, M, N, K, stream)
+
+
+def gemm_a8w8_b128_grouped_bf16(qa, sa, a_rows, qw, sw, y, offsets, rows, G, T, N, K, stream=None) -> int:
+    return lib().gemm_a8w8_b128_grouped_bf16(qa, sa, a_rows, qw, sw, y, offsets, rows, G, T, N, K, stream)
 
 
 # ------------------------------------------------------------------ tensor helpers
@@ -326,3 +358,185 @@ def linear_a8w8(x, qw, sw):
     """The A8W8 layer: dynamic per-token FP8 quantization of BF16 x, then the PTPC GEMM."""
     qa, sa = quant_act_ptpc(x)
     return gemm_a8w8(qa, sa, qw, sw)
+
+
+# ------------------------------------------------------------------ block-128 FP8
+def _raw_stream(device):
+    """The current stream's handle on `device`, which must be the current device: the library launches there."""
+    torch = _torch()
+    if device.index != torch.cuda.current_device():
+        raise ValueError("operands are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _same_device(like, **others):
+    for name, t in others.items():
+        if t is not None and t.device != like.device:
+            raise ValueError("%s must be on %s, got %s" % (name, like.device, t.device))
+
+
+def quant_act_b128(x, q=None, s=None):
+    """BF16 [M, K] -> (E4M3fn codes uint8 [M, K], FP32 scales [M, K/128]), one scale per 128 K-values of a row."""
+    torch = _torch()
+    _need(x, torch.bfloat16, 2, "x")
+    M, K = x.shape
+    q = _out(q, torch.uint8, (M, K), x, "q")
+    s = _out(s, torch.float32, (M, K // 128), x, "s")
+    _ok(lib().b128_quant_act_fp8(x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(), _raw_stream(x.device)),
+        "b128_quant_act_fp8")
+    return q, s
+
+
+def quant_weight_b128(w):
+    """FP32 [N, K] -> (E4M3fn codes uint8 [N, K], FP32 scales [ceil(N/128), K/128]), one scale per 128 x 128."""
+    torch = _torch()
+    _need(w, torch.float32, 2, "w")
+    N, K = w.shape
+    q = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+    s = torch.empty(((N + 127) // 128, K // 128), dtype=torch.float32, device=w.device)
+    _ok(lib().b128_quant_weight_f32(w.data_ptr(), N, K, q.data_ptr(), s.data_ptr(), _raw_stream(w.device)),
+        "b128_quant_weight_f32")
+    return q, s
+
+
+def gemm_a8w8_b128(qa, sa, qw, sw, y=None):
+    """Block-128 FP8: codes [M, K] with scales [M, K/128], codes [N, K] with scales [ceil(N/128), K/128]
+    -> BF16 Y [M, N] = A . W^T."""
+    torch = _torch()
+    _need(qa, torch.uint8, 2, "qa")
+    _need(sa, torch.float32, 2, "sa")
+    _need(qw, torch.uint8, 2, "qw")
+    _need(sw, torch.float32, 2, "sw")
+    M, K = qa.shape
+    N = qw.shape[0]
+    if qw.shape[1] != K or sa.shape != (M, K // 128) or sw.shape != ((N + 127) // 128, K // 128):
+        raise ValueError("inconsistent block-128 A8W8 operand shapes")
+    _same_device(qa, sa=sa, qw=qw, sw=sw)
+    y = _out(y, torch.bfloat16, (M, N), qa, "y")
+    _ok(lib().gemm_a8w8_b128_bf16(qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(), y.data_ptr(), M, N, K,
+                                  _raw_stream(qa.device)), "gemm_a8w8_b128_bf16")
+    return y
+
+
+def linear_a8w8_b128(x, qw, sw):
+    """The block-128 FP8 layer: dynamic quantization of BF16 x (one scale per 128 values), then the GEMM."""
+    qa, sa = quant_act_b128(x)
+    return gemm_a8w8_b128(qa, sa, qw, sw)
+
+
+def gemm_a8w8_b128_grouped(qa, sa, qw, sw, offsets, rows=None, y=None):
+    """Grouped block-128 FP8 GEMM over experts: codes [R, K] / scales [R, K/128], stacked expert weights
+    [G, N, K] / [G, ceil(N/128), K/128], offsets int32 [G + 1] (device) -> BF16 Y [T, N], rows offsets[e] ..
+    offsets[e+1]-1 multiplied with expert e; rows of Y outside every group are not written.  rows (int32 [T],
+    device, e.g. from moe_route) names the row of qa / sa that feeds each row of Y (a row of zeros where it
+    is out of range); without it T = R."""
+    torch = _torch()
+    _need(qa, torch.uint8, 2, "qa")
+    _need(sa, torch.float32, 2, "sa")
+    _need(qw, torch.uint8, 3, "qw")
+    _need(sw, torch.float32, 3, "sw")
+    _need(offsets, torch.int32, 1, "offsets")
+    if rows is not None:
+        _need(rows, torch.int32, 1, "rows")
+    R, K = qa.shape
+    G, N = qw.shape[0], qw.shape[1]
+    T = R if rows is None else rows.shape[0]
+    if (qw.shape[2] != K or sa.shape != (R, K // 128) or sw.shape != (G, (N + 127) // 128, K // 128)
+            or offsets.shape[0] != G + 1):
+        raise ValueError("inconsistent grouped block-128 A8W8 operand shapes")
+    _same_device(qa, sa=sa, qw=qw, sw=sw, offsets=offsets, rows=rows)
+    y = _out(y, torch.bfloat16, (T, N), qa, "y")
+    _ok(lib().gemm_a8w8_b128_grouped_bf16(qa.data_ptr(), sa.data_ptr(), R, qw.data_ptr(), sw.data_ptr(), y.data_ptr(),
+                                          offsets.data_ptr(), rows.data_ptr() if rows is not None else None, G, T, N, K,
+                                          _raw_stream(qa.device)), "gemm_a8w8_b128_grouped_bf16")
+    return y
+
+
+# ------------------------------------------------------------------ expert routing
+def moe_route_workspace_bytes(T, top, E) -> int:
+    return lib().moe_route_workspace_bytes(T, top, E)
+
+
+def moe_balance_loss_workspace_bytes(T, E) -> int:
+    return lib().moe_balance_loss_workspace_bytes(T, E)
+
+
+def _scratch(nbytes, device):
+    """Memory for one call, from torch's allocator, which keeps it apart from calls on other streams and in
+    captured graphs."""
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device) if nbytes else None
+
+
+def moe_route(ids, experts):
+    """Expert ids int32 or int64 [T, top] (a value outside 0 .. experts - 1 is no choice) -> int32 counts [E],
+    offsets [E + 1], rows [T * top] (the token of every packed row, -1 behind the last) and slots [T, top] (the
+    packed row of every choice, -1 for no choice).  Packed rows are sorted by expert, then token."""
+    torch = _torch()
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be an int32 or int64 torch.Tensor")
+    _need(ids, ids.dtype, 2, "ids")
+    T, top = ids.shape
+    counts = torch.empty(experts, dtype=torch.int32, device=ids.device)
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+    rows = torch.empty(T * top, dtype=torch.int32, device=ids.device)
+    slots = torch.empty((T, top), dtype=torch.int32, device=ids.device)
+    need = lib().moe_route_workspace_bytes(T, top, experts)
+    ws = _scratch(need, ids.device)
+    _ok(lib().moe_route(ids.data_ptr(), ids.element_size(), T, top, experts, counts.data_ptr(), offsets.data_ptr(),
+                        rows.data_ptr(), slots.data_ptr(), ws.data_ptr() if need else None, need,
+                        _raw_stream(ids.device)), "moe_route")
+    return counts, offsets, rows, slots
+
+
+def _router_args(logits, mask):
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be a float32 or bfloat16 torch.Tensor")
+    _need(logits, logits.dtype, 2, "logits")
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError("mask must be a bool or uint8 torch.Tensor")
+        _need(mask, mask.dtype, 1, "mask")
+        if mask.shape[0] != logits.shape[0]:
+            raise ValueError("mask must have one entry per row of logits")
+        _same_device(logits, mask=mask)
+    return MX_F32 if logits.dtype == torch.float32 else MX_BF16
+
+
+def moe_balance_loss(logits, counts, coef, mask=None):
+    """Balance loss coef * E * sum_e f_e P_e of a router: logits [T, E] (float32 or bfloat16), counts int32 [E]
+    from moe_route, mask [T] (0 / False marks a padded token) -> (loss float32 [1], weights float32 [E] for
+    moe_balance_loss_grad)."""
+    torch = _torch()
+    dtype = _router_args(logits, mask)
+    _need(counts, torch.int32, 1, "counts")
+    T, E = logits.shape
+    if counts.shape[0] != E:
+        raise ValueError("counts must have one entry per expert")
+    _same_device(logits, counts=counts)
+    loss = torch.empty(1, dtype=torch.float32, device=logits.device)
+    weights = torch.empty(E, dtype=torch.float32, device=logits.device)
+    need = lib().moe_balance_loss_workspace_bytes(T, E)
+    ws = _scratch(need, logits.device)
+    _ok(lib().moe_balance_loss(logits.data_ptr(), dtype, T, E, counts.data_ptr(),
+                               mask.data_ptr() if mask is not None else None, coef, loss.data_ptr(), weights.data_ptr(),
+                               ws.data_ptr() if need else None, need, _raw_stream(logits.device)), "moe_balance_loss")
+    return loss, weights
+
+
+def moe_balance_loss_grad(logits, weights, grad_loss, mask=None, dlogits=None):
+    """Gradient of moe_balance_loss with respect to the logits, times grad_loss (float32 [1], device), in the
+    logits' type; weights come from moe_balance_loss, mask is the same one."""
+    torch = _torch()
+    dtype = _router_args(logits, mask)
+    _need(weights, torch.float32, 1, "weights")
+    _need(grad_loss, torch.float32, 1, "grad_loss")
+    T, E = logits.shape
+    if weights.shape[0] != E or grad_loss.shape[0] != 1:
+        raise ValueError("weights must have one entry per expert and grad_loss one entry")
+    _same_device(logits, weights=weights, grad_loss=grad_loss)
+    dlogits = _out(dlogits, logits.dtype, (T, E), logits, "dlogits")
+    _ok(lib().moe_balance_loss_grad(logits.data_ptr(), dtype, T, E, weights.data_ptr(),
+                                    mask.data_ptr() if mask is not None else None, grad_loss.data_ptr(),
+                                    dlogits.data_ptr(), _raw_stream(logits.device)), "moe_balance_loss_grad")
+    return dlogits

@@ -65,6 +65,9 @@ typedef enum {
     MX_ERROR_DEVICE = 6             /* the current device is not a gfx950 GPU             */
 } mx_status;
 
+/* Type of a router's logits. */
+typedef enum { MX_F32 = 0, MX_BF16 = 1 } mx_dtype;
+
 /* Version of this interface (incremented on any ABI change). */
 int mx_abi_version(void);
 
@@ -269,6 +272,112 @@ size_t gemm_a8w8_ptpc_workspace_bytes(int64_t M, int64_t N, int64_t K);
 mx_status gemm_a8w8_ptpc_bf16(const void *qa, const float *sa, const void *qw, const float *sw,
                               void *y_bf16, int64_t M, int64_t N, int64_t K,
                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Block-128 FP8: E4M3 codes with one FP32 scale for each block of 128 values.
+ * An activation block is 128 consecutive K-values of one row, a weight block
+ * 128 rows x 128 K-values (the last row block may be short).  Per block:
+ * a = max|x|, s = fl32(a / 448), s = 1 where that is 0, code = E4M3fn
+ * round-to-nearest-even of fl32(x / s), saturating at 448; a block with NaN/Inf
+ * gets s = NaN and every code 0x7F.  K > 0 and K % 128 == 0; M, N >= 0.
+ *
+ *   b128_quant_act_fp8: x_bf16 [M, K] in (16-byte aligned); q [M, K] out (8-byte
+ *     aligned); s [M, K/128] FP32 out (4-byte aligned).
+ *   b128_quant_weight_f32: w [N, K] FP32 in (16-byte aligned); q [N, K] out
+ *     (4-byte aligned); s [ceil(N/128), K/128] FP32 out.
+ */
+mx_status b128_quant_act_fp8(const void *x_bf16, int64_t M, int64_t K,
+                             void *q, float *s, void *stream);
+mx_status b128_quant_weight_f32(const float *w, int64_t N, int64_t K,
+                                void *q, float *s, void *stream);
+
+/*
+ * Block-128 A8W8 GEMM, BF16 out:
+ *   Y[m,n] = sum_b sa[m,b] * sw[n/128,b] * sum_{k in block b} e4m3(qa[m,k]) * e4m3(qw[n,k])
+ *   qa [M, K], sa [M, K/128]; qw [N, K], sw [ceil(N/128), K/128]; y_bf16 [M, N].
+ * K > 0 and K % 128 == 0; any M, N.  qa, qw 16-byte aligned; sa, sw 4-byte
+ * aligned; y_bf16 2-byte aligned.  No workspace; calls on different streams may
+ * overlap.  Results do not depend on timing.
+ * The products of one block are added by an FP8 MFMA, which cuts each product at
+ * 2^-13 of the largest of its group of eight; everything else is added in
+ * FP32.  |y - exact| <= 2^-8 |exact| + 2^-10 sum|a w| for any codes, with a and w
+ * the dequantized operands; for products of mixed sign and like size, the usual
+ * case, 2^-14 takes the place of 2^-10.  The scale product
+ * sa * sw is formed in FP32: where it is below 2^-126 it is rounded to a
+ * subnormal number, and beyond FP32's range it is an infinity.
+ */
+mx_status gemm_a8w8_b128_bf16(const void *qa, const float *sa, const void *qw, const float *sw,
+                              void *y_bf16, int64_t M, int64_t N, int64_t K, void *stream);
+
+/*
+ * Grouped block-128 A8W8 GEMM over MoE experts: rows offsets[e] ..
+ * offsets[e+1]-1 of Y are products with expert weight e.
+ *   qa [a_rows, K], sa [a_rows, K/128]; qw [G, N, K], sw [G, ceil(N/128), K/128];
+ *   y_bf16 [T, N] out; rows outside every group are not written.
+ *   offsets [G + 1] int32, DEVICE memory, non-decreasing, offsets[0] = 0 (e.g.
+ *            from moe_route): read by the kernel, so the call needs no host
+ *            round trip and can be captured.  Values outside 0 .. T count as the
+ *            nearer end.
+ *   rows     [T] int32, DEVICE memory, or NULL: row r of Y comes from row rows[r]
+ *            of A (e.g. the token of a packed row, from moe_route, so tokens are
+ *            quantized once and never copied); a value outside 0 .. a_rows - 1
+ *            gives a row of zeros.  NULL: row r of A, a_rows >= T.
+ * K % 128 == 0; G <= 65535; alignments and precision as gemm_a8w8_b128_bf16, offsets and rows
+ * 4-byte aligned.  T / G, the mean group, picks the kernel; every row of every
+ * group is written whatever the groups' sizes.  G, T or N == 0: no-op.
+ */
+mx_status gemm_a8w8_b128_grouped_bf16(const void *qa, const float *sa, int64_t a_rows, const void *qw,
+                                      const float *sw, void *y_bf16, const int32_t *offsets,
+                                      const int32_t *rows, int64_t G, int64_t T, int64_t N, int64_t K,
+                                      void *stream);
+
+/*
+ * From a router's choices to the grouped GEMMs' packed rows.
+ *   ids [T, top] in, int32 (id_bytes 4) or int64 (8): the expert of every choice;
+ *       a value outside 0 .. E - 1 (e.g. -1, a padded token) is no choice.
+ *   counts  [E] int32 out: choices of every expert
+ *   offsets [E + 1] int32 out: their running sum, from 0
+ *   rows    [T * top] int32 out: the token of every packed row, -1 behind the last
+ *   slots   [T, top] int32 out: the packed row of every choice, -1 for no choice
+ * Packed rows are sorted by expert, then token, then place in ids' row.
+ * 1 <= E <= 1024, T * top <= 2^24.  workspace: moe_route_workspace_bytes(T, top,
+ * E) bytes, 16-byte aligned, any content before and after (NULL when that is 0);
+ * calls that may overlap need workspaces of their own.
+ */
+size_t moe_route_workspace_bytes(int64_t T, int64_t top, int64_t E);
+mx_status moe_route(const void *ids, int id_bytes, int64_t T, int64_t top, int64_t E,
+                    int32_t *counts, int32_t *offsets, int32_t *rows, int32_t *slots,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Balance loss of a router, from its logits and the per-expert counts of
+ * moe_route:
+ *   loss = coef * E * sum_e f_e P_e, f_e = counts_e / sum(counts),
+ *   P_e = mean over the unmasked tokens of softmax(logits[t])_e.
+ *   logits [T, E] in, FP32 or BF16; counts [E] in; mask [T] bytes in or NULL: 0 marks
+ *   a padded token, whose logits are not read
+ *   loss [1] FP32 out; weights [E] FP32 out: coef * E * f_e / (unmasked tokens),
+ *   what moe_balance_loss_grad needs.
+ * No choice or no unmasked token at all: loss and weights 0.  A row whose logits
+ * are all -infinity has no probabilities (all 0) but counts as a token; a NaN or
+ * +infinity in an unmasked row makes the loss NaN.
+ * 1 <= E <= 1024, T < 2^31.  workspace as for moe_route.
+ */
+size_t moe_balance_loss_workspace_bytes(int64_t T, int64_t E);
+mx_status moe_balance_loss(const void *logits, mx_dtype dtype, int64_t T, int64_t E,
+                           const int32_t *counts, const uint8_t *mask, float coef,
+                           float *loss, float *weights,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of the balance loss with respect to the logits (the counts are whole
+ * numbers and carry none), times grad_loss [1] (FP32, device):
+ *   dlogits[t,e] = grad_loss * p_te * (weights_e - sum_j weights_j p_tj),
+ * 0 for masked tokens.  dlogits [T, E] out in the logits' type.
+ */
+mx_status moe_balance_loss_grad(const void *logits, mx_dtype dtype, int64_t T, int64_t E,
+                                const float *weights, const uint8_t *mask, const float *grad_loss,
+                                void *dlogits, void *stream);
 
 #ifdef __cplusplus
 }
