@@ -222,9 +222,18 @@ MX_API mx_status b128_quant_weight_f32(const float* w, int64_t N, int64_t K, voi
     return launched(mx::launch_quant_b128_weight(w, N, K, q, s, reinterpret_cast<hipStream_t>(stream)));
 }
 
+// K <= 2^22: a tile's rows are reached by 32-bit offsets; tiles of at least 32 x 64 must fit one 1-D grid
+static mx_status check_gemm_b128(int64_t M, int64_t N, int64_t K) {
+    const mx_status st = check_gemm(M, N, K);
+    if (st != MX_SUCCESS) return st;
+    if (K > (INT64_C(1) << 22)) return MX_ERROR_UNSUPPORTED_SHAPE;
+    if ((M + 31) / 32 > INT32_MAX / ((N + 63) / 64 > 0 ? (N + 63) / 64 : 1)) return MX_ERROR_UNSUPPORTED_SHAPE;
+    return MX_SUCCESS;
+}
+
 MX_API mx_status gemm_a8w8_b128_bf16(const void* qa, const float* sa, const void* qw, const float* sw, void* y_bf16,
                                      int64_t M, int64_t N, int64_t K, void* stream) {
-    mx_status st = check_gemm(M, N, K);
+    mx_status st = check_gemm_b128(M, N, K);
     if (st != MX_SUCCESS) return st;
     if (M == 0 || N == 0) return MX_SUCCESS;
     if (!qa || !sa || !qw || !sw || !y_bf16) return MX_ERROR_INVALID_VALUE;
@@ -237,13 +246,15 @@ MX_API mx_status gemm_a8w8_b128_bf16(const void* qa, const float* sa, const void
 MX_API mx_status gemm_a8w8_b128_grouped_bf16(const void* qa, const float* sa, int64_t a_rows, const void* qw,
                                              const float* sw, void* y_bf16, const int32_t* offsets, const int32_t* rows,
                                              int64_t G, int64_t T, int64_t N, int64_t K, void* stream) {
-    mx_status st = check_gemm(T, N, K);
+    mx_status st = check_gemm_b128(T, N, K);
     if (st != MX_SUCCESS) return st;
     if (G < 0 || a_rows < 0) return MX_ERROR_INVALID_VALUE;
     if (G > 65535 || a_rows > (INT64_C(1) << 40) / K || N > (INT64_C(1) << 40) / K / (G > 0 ? G : 1))
         return MX_ERROR_UNSUPPORTED_SHAPE;
-    // 128-row tiles, one partial tile per group, must fit one 1-D grid
-    if ((T / 128 + (G < T ? G : T)) * ((N + 127) / 128) > INT32_MAX) return MX_ERROR_UNSUPPORTED_SHAPE;
+    // tiles of at least 32 x 64, one partial row tile per group, must fit one 1-D grid
+    if ((T / 32 + (G < T ? G : T)) > INT32_MAX / ((N + 63) / 64 > 0 ? (N + 63) / 64 : 1)) return MX_ERROR_UNSUPPORTED_SHAPE;
+    // named rows are reached by 32-bit offsets
+    if (rows && a_rows > (INT64_C(1) << 32) / K - 1) return MX_ERROR_UNSUPPORTED_SHAPE;
     if (G == 0 || T == 0 || N == 0) return MX_SUCCESS;
     if (!qa || !sa || !qw || !sw || !y_bf16 || !offsets) return MX_ERROR_INVALID_VALUE;
     if (a_rows == 0 || (!rows && a_rows < T)) return MX_ERROR_INVALID_VALUE;

@@ -1,0 +1,548 @@
+// gemm_b128.hpp - kernels of the A8W8 GEMM with one FP32 scale per block of 128, dense and grouped over experts.
+//
+//   Y[m, n] = sum_b sa[m, b] sw[n / 128, b] P_b[m, n],   P_b[m, n] = sum_{k in block b} qa[m, k] qw[n, k]
+//
+// with E4M3 codes and b the 128-value blocks of K.  P_b is one FP8 MFMA of depth 128 started from zero;
+// the scaled sum over blocks runs in FP32 on the vector ALU: acc = fma(P_b, sa sw, acc).
+//
+// Precision.  The FP8 MFMA adds the 128 products of a block in groups of eight, and cuts each product at 2^-13
+// of the power of two of its group's largest one (measured on this GPU, toward zero); the groups are added
+// with FP32's width.  So a block's sum is off by less than 7 * 2^-13 of the sum of its products' magnitudes whatever the
+// codes, and by 2^-15.5 at most over a million outputs of quantized normal values, 2^-19 in the mean: far
+// below the rounding of the BF16 output except for strongly cancelling sums.  The per-row-scale GEMM of this
+// library widens its codes to FP16 instead, which is exact up to FP32 but runs at half the matrix rate; with a
+// scale per block, blocks have to leave the MFMA for their FP32 sum anyway, and the FP8 rate is kept.
+//
+// Operand layout: lane l holds row l % 16 of a fragment and, of the block's eight 16-byte chunks, chunks
+// l / 16 and l / 16 + 4.  Both operands use the same order, and the order of K inside a block does not
+// matter, so a wave's two loads of a fragment each take 64 contiguous bytes per row.  Weights are the
+// first operand: a lane's four results are four consecutive n of one m, which share one activation scale.
+#pragma once
+
+#include "mx_device.hpp"
+
+namespace mx {
+namespace b128 {
+
+constexpr int kFmtE4M3 = 0;  // scaled-MFMA operand format; scale operands 0 select the MFMA without scales
+
+__device__ __forceinline__ v8i operand(uint4 lo, uint4 hi) {
+    v8i r = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    return r;
+}
+__device__ __forceinline__ v8i operand(v4u lo, v4u hi) {
+    v8i r = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    return r;
+}
+// 16 x 16 products of one block, from zero
+__device__ __forceinline__ v4f block_mfma(v8i w, v8i x) {
+    const v4f z = {0.f, 0.f, 0.f, 0.f};
+    return mfma16<kFmtE4M3, 0>(w, x, z, 0, 0);
+}
+
+// 16 or 4 bytes per lane from a buffer straight into LDS: lane i of the wave writes lds_base + 16 i or 4 i.
+__device__ __forceinline__ void buffer2lds16(__amdgpu_buffer_rsrc_t r, void* lds_base, uint32_t lane_offset, int offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds_base, 16, lane_offset, offset, 0, 0);
+}
+__device__ __forceinline__ void buffer2lds4(__amdgpu_buffer_rsrc_t r, void* lds_base, uint32_t lane_offset, int offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds_base, 4, lane_offset, offset, 0, 0);
+}
+
+struct Args {
+    const uint8_t* qa;      // [rows of A, K]
+    const float* sa;        // [rows of A, K / 128]
+    const uint8_t* qw;      // [groups, N, K]
+    const float* sw;        // [groups, ceil(N / 128), K / 128]
+    uint16_t* y;            // [M, N]
+    const int32_t* offsets; // grouped: [G + 1], else null
+    const int32_t* rows;    // grouped: A row of every Y row, or null (the same row)
+    int64_t arows;          // rows of A
+    int64_t M, N, K;
+    int G;
+};
+
+// Rows r0 .. r1 - 1 of Y belong to group e.  Offsets that are out of order or past M give fewer rows, never
+// rows outside Y.
+__device__ __forceinline__ void group_rows(const Args& a, int e, int64_t& r0, int64_t& r1) {
+    r0 = min((int64_t)max(a.offsets[e], 0), a.M);
+    r1 = min((int64_t)max(a.offsets[e + 1], 0), a.M);
+}
+// The A row that feeds row r of Y, -1 if there is none (its outputs are 0)
+__device__ __forceinline__ int64_t a_row(const Args& a, int64_t r) {
+    if (a.rows == nullptr) return r;
+    const int64_t t = a.rows[r];
+    return t >= 0 && t < a.arows ? t : -1;
+}
+__device__ __forceinline__ void store4(uint16_t* y, int64_t N, int64_t n, v4f v, bool vec) {
+    uint16_t* dst = y + n;
+    if (vec && n + 3 < N) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < N) dst[i] = (uint16_t)bf16_rne(v[i]);
+    }
+}
+
+// ---------------------------------------------------------------------------- few rows
+// One workgroup per 16 FN columns (and group); its W waves take contiguous parts of K and meet in LDS, summed in
+// wave order.  Operands go from memory to registers through a ring of D stages of one block; rows in chunks
+// of at most 16 FM.
+template <int FM, int FN>
+struct Stage {
+    uint4 w[FN][2], x[FM][2];
+    float sw[FN], sx[FM];
+};
+
+template <int FM, int FN, int W, int D>
+__global__ __launch_bounds__(64 * W) void rows_kernel(Args a) {
+    __shared__ v4f red[W][FN][FM][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, g = lane >> 4;
+    const int nkb = (int)(a.K / 128), per = (nkb + W - 1) / W;
+    const int kb0 = min(wave * per, nkb), nk = min(per, nkb - kb0);
+    const int64_t n0 = (int64_t)blockIdx.x * 16 * FN;
+    const int e = blockIdx.y;
+    int64_t r0 = 0, r1 = a.M;
+    if (a.offsets) group_rows(a, e, r0, r1);
+    const uint8_t* wp[FN];
+    const float* swp[FN];
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+        const int64_t n = min(n0 + 16 * f + l16, a.N - 1);
+        wp[f] = a.qw + (e * a.N + n) * a.K + 16 * g + (int64_t)kb0 * 128;
+        swp[f] = a.sw + (e * ((a.N + 127) / 128) + min(n0 + 16 * f, a.N - 1) / 128) * nkb + kb0;
+    }
+    // rows m0 .. of a chunk with F fragments
+    auto chunk = [&](int64_t m0, auto fc) __attribute__((always_inline)) {
+        constexpr int F = decltype(fc)::value;
+        const uint8_t* ap[F];
+        const float* sap[F];
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const int64_t r = max(a_row(a, min(m0 + 16 * j + l16, r1 - 1)), (int64_t)0);
+            ap[j] = a.qa + r * a.K + 16 * g + (int64_t)kb0 * 128;
+            sap[j] = a.sa + r * nkb + kb0;
+        }
+        v4f acc[FN][F] = {};
+        Stage<F, FN> st[D];
+        auto load = [&](Stage<F, FN>& s, int i) __attribute__((always_inline)) {
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                s.w[f][0] = ldg16(wp[f] + i * 128);
+                s.w[f][1] = ldg16(wp[f] + i * 128 + 64);
+                s.sw[f] = swp[f][i];
+            }
+#pragma unroll
+            for (int j = 0; j < F; ++j) {
+                s.x[j][0] = ldg16(ap[j] + i * 128);
+                s.x[j][1] = ldg16(ap[j] + i * 128 + 64);
+                s.sx[j] = sap[j][i];
+            }
+        };
+        auto compute = [&](const Stage<F, FN>& s) __attribute__((always_inline)) {
+#pragma unroll
+            for (int f = 0; f < FN; ++f)
+#pragma unroll
+                for (int j = 0; j < F; ++j) {
+                    const v4f p = block_mfma(operand(s.w[f][0], s.w[f][1]), operand(s.x[j][0], s.x[j][1]));
+                    const float sc = s.sx[j] * s.sw[f];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[f][j][i] = __builtin_fmaf(p[i], sc, acc[f][j][i]);
+                }
+        };
+        if (nk > 0) {
+            static_for<D - 1>([&](auto d) { load(st[decltype(d)::value], min((int)decltype(d)::value, nk - 1)); });
+            int i = 0;
+            for (; i + 2 * D - 2 < nk; i += D)  // every load of the round is of this wave's part
+                static_for<D>([&](auto dc) {
+                    constexpr int d = decltype(dc)::value;
+                    load(st[(d + D - 1) % D], i + d + D - 1);
+                    __builtin_amdgcn_sched_barrier(0);  // keep the load ahead of the products, D - 1 stages in flight
+                    compute(st[d]);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+            for (; i < nk; i += D)
+                static_for<D>([&](auto dc) {
+                    constexpr int d = decltype(dc)::value;
+                    if (i + d < nk) {
+                        if (i + d + D - 1 < nk) load(st[(d + D - 1) % D], i + d + D - 1);
+                        compute(st[d]);
+                    }
+                });
+        }
+#pragma unroll
+        for (int f = 0; f < FN; ++f)
+#pragma unroll
+            for (int j = 0; j < F; ++j) red[wave][f][j][lane] = acc[f][j];
+        __syncthreads();
+        for (int t = threadIdx.x; t < FN * F * 64; t += 64 * W) {
+            const int f = t / (F * 64), j = t / 64 % F, l = t % 64;
+            v4f s = red[0][f][j][l];
+#pragma unroll
+            for (int w = 1; w < W; ++w) s += red[w][f][j][l];
+            const int64_t m = m0 + 16 * j + (l & 15);
+            if (m < r1) {
+                const v4f zero = {0.f, 0.f, 0.f, 0.f};
+                store4(a.y + m * a.N, a.N, n0 + 16 * f + 4 * (l >> 4), a_row(a, m) >= 0 ? s : zero,
+                       a.N % 4 == 0 && ((uintptr_t)a.y & 7) == 0);
+            }
+        }
+        __syncthreads();
+    };
+    for (int64_t m0 = r0; m0 < r1; m0 += 16 * FM) {
+        const int left = (int)min((r1 - m0 + 15) / 16, (int64_t)FM);
+        static_for<FM>([&](auto fc) {
+            constexpr int F = decltype(fc)::value + 1;
+            if (left == F) chunk(m0, std::integral_constant<int, F>{});
+        });
+    }
+}
+
+// ---------------------------------------------------------------------------- many rows
+// A TM x TN = 16 FM WM x 16 FN WN output tile per workgroup.  KG groups of WM x WN waves take every KG-th block of
+// K (group q blocks q, q + KG, ...) and are summed in group order at the end; a step is one block per group.  Operands
+// pass through a ring of S slots in LDS, filled by direct copies.
+//
+// Slot, per group: TM + TN rows of 128 bytes, chunk c of row r at place c ^ (r / 2 % 8), so that the 16 lanes of a
+// fragment's read touch 16 different bank groups.  Scales come in batches of eight blocks, three of them in
+// LDS: a copy takes 32 bytes from each of eight rows, and the copies of batch B travel with the codes of the
+// steps of batch B - 1, one per wave and step.  (Copying each step's scales, one 4-byte piece of a cache line per
+// row, took as many line requests as the codes.)
+//
+// Step u of a wave, its first two weight fragments, its row fragments and its scales already in registers:
+//   1. weight fragments 0 .. FN - 3 times all row fragments, reading weight fragment f + 2 before fragment f is used;
+//   2. every operand of the step is now in registers: wait for the copies of u + 1, one barrier;
+//   3. the last two weight fragments, row fragment by row fragment, reading the next step's scales, first two weight
+//      fragments and row fragments as registers fall free.
+// So MFMAs run across the barrier.  The slot that the barrier frees is refilled with the copies of u + S, spread over the
+// MFMAs of 3 and of the next step's 1: issued in one burst they hold up the waves behind the address unit.  The FMAs that scale a product follow two
+// MFMAs behind it.
+//
+// LDS reads are inline assembly (the compiler would drain the copies before each one).  The compiler takes their
+// results for ready at once, so nothing may touch a result register before the wait that covers it: every wait ties its
+// results, and what is carried into the next step is waited for and tied before the step ends, ahead of any
+// register copy the loop may need.  test_isa_hazards_b128.py checks that in the assembly.
+struct TileAt {
+    int e;            // group
+    int64_t m0, r1;   // first row, end of the group's rows
+    int64_t n0;
+    int tm, tn;       // row and column tile
+    bool live;
+};
+
+// Workgroup b's tile.  Consecutive workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of tiles,
+// and walks it in bands of four row tiles, so tiles that run together share operand panels in its L2.
+template <int TM, int TN>
+__device__ __forceinline__ TileAt tile_of(const Args& a, int b, int tiles_m, int tiles_n) {
+    const int T = tiles_m * tiles_n, T8 = T & ~7;
+    const int L = b < T8 ? (b & 7) * (T8 >> 3) + (b >> 3) : b;
+    const int band = L / (4 * tiles_n), high = min(tiles_m - 4 * band, 4), rem = L - band * 4 * tiles_n;
+    int tm = 4 * band + rem % high;
+    TileAt t = {0, (int64_t)tm * TM, a.M, (int64_t)(rem / high) * TN, tm, rem / high, true};
+    if (a.offsets == nullptr) return t;
+    const int lane = threadIdx.x & 63;
+    t.live = false;
+    for (int g0 = 0; g0 < a.G; g0 += 64) {  // 64 groups at a time: running sum of their row tiles
+        int64_t r0 = 0, r1 = 0;
+        if (g0 + lane < a.G) group_rows(a, g0 + lane, r0, r1);
+        const int n = r1 > r0 ? (int)((r1 - r0 + TM - 1) / TM) : 0;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(sum, d);
+            if (lane >= d) sum += o;
+        }
+        const uint64_t past = __ballot(sum > tm);
+        if (past) {
+            const int i = __builtin_ctzll(past);
+            t.e = __builtin_amdgcn_readfirstlane(g0 + i);
+            const int first = __shfl((int)r0, i), end = __shfl((int)r1, i), before = __shfl(sum - n, i);
+            t.m0 = __builtin_amdgcn_readfirstlane(first) + (int64_t)__builtin_amdgcn_readfirstlane(tm - before) * TM;
+            t.r1 = __builtin_amdgcn_readfirstlane(end);
+            t.live = true;
+            break;
+        }
+        tm -= __shfl(sum, 63);
+    }
+    return t;
+}
+
+template <int FM, int FN, int WM, int WN, int KG, int S>
+__global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void tile_kernel(Args a, int tiles_m, int tiles_n) {
+    constexpr int TM = 16 * FM * WM, TN = 16 * FN * WN, W = WM * WN * KG;
+    constexpr int CA = (KG * TM / 8 + W - 1) / W, CW = (KG * TN / 8 + W - 1) / W;  // copies of eight rows per wave
+    constexpr bool kAhead = S == 2 && TM * TN >= 256 * 128;                        // lines fetched ahead into L2
+    constexpr int C = CA + CW + 1 + kAhead;                                        // and one of scales
+    constexpr int kPart = (TM + TN) * 128, kSlot = KG * kPart, kBatch = (TM + 8) * 32, kBatches = S * kSlot;
+    constexpr int kTable = kBatches + 3 * kBatch, kSink = kTable + (TM + 8) * 4, kLds = kSink + (kAhead ? 256 : 0);
+    constexpr int SB = 8 / KG;  // steps per batch of scales
+    // MFMAs of a step, and those ahead of its barrier; the copies issued behind the barrier that frees their slot (the
+    // others follow in the next step, ahead of its barrier), and the MFMAs that those others are spread over
+    constexpr int kMf = FN * FM, kFirst = (FN - 2) * FM;
+    constexpr int kWish = kFirst == 0 ? C : kFirst >= 2 * C ? FM : 2 * FM, kEarly = kWish < C ? kWish : C;
+    constexpr int kLate = C - kEarly, kSpan = 2 * kLate < kFirst ? 2 * kLate : kFirst;
+    constexpr bool kOneBlock = 128 % (16 * FN) == 0;    // a wave's columns lie in one weight block
+    constexpr int kFree = FM > 2 && FN < 8 ? 2 : FM > 1 ? 1 : 0;  // row fragments read into registers of their own
+    static_assert(TM / 8 + 1 <= SB * W && S <= SB, "a batch's copies in its steps, and its place free in time");
+    static_assert(kLds <= 160 * 1024 && (S - 1) * C < 64 && FN >= 2 && FN <= 8, "LDS, counters, weight scales");
+    static_assert((KG - 1) * FM * FN * 1024 * WM * WN <= kBatches, "sums of the groups");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, g = lane >> 4, kg = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
+    const int nkb = __builtin_amdgcn_readfirstlane((int)(a.K / 128)), steps = (nkb + KG - 1) / KG;
+    const TileAt t = tile_of<TM, TN>(a, blockIdx.x, tiles_m, tiles_n);
+    if (!t.live) return;
+    const int64_t nblocks = (a.N + 127) / 128, nb0 = t.n0 / 128;
+
+    // Copies are buffer loads: a 32-bit offset per lane, the block of K in the scalar offset.  Rows are counted from the
+    // tile's first one, or from A's where a table names them.
+    const int64_t arow0 = a.rows ? 0 : t.m0;
+    constexpr int kRawWord3 = 0x00020000;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(a.qa + arow0 * a.K), (short)0, -1, kRawWord3);
+    const __amdgpu_buffer_rsrc_t rw =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(a.qw + (t.e * a.N + t.n0) * a.K), (short)0, -1, kRawWord3);
+    const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc((void*)(a.sa + arow0 * nkb), (short)0, -1, kRawWord3);
+    const __amdgpu_buffer_rsrc_t rsw =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(a.sw + (t.e * nblocks + nb0) * nkb), (short)0, -1, kRawWord3);
+    auto tile_row = [&](int i) { return (uint32_t)(max(a_row(a, min(t.m0 + i, t.r1 - 1)), (int64_t)0) - arow0); };
+
+    // offsets of the rows of the scale copies: the tile's A rows, then weight blocks
+    uint32_t* table = reinterpret_cast<uint32_t*>(lds + kTable);
+    for (int i = threadIdx.x; i < TM + 8; i += 64 * W)
+        table[i] = (i < TM ? tile_row(i) : (uint32_t)min((int64_t)i - TM, nblocks - 1 - nb0)) * (uint32_t)nkb * 4;
+
+    // code copy i: eight rows of one group's block, a 16-byte chunk per lane.  Every wave issues C copies a step, so that
+    // one count serves them all; where they do not divide, some repeat the last.
+    uint32_t src[CA + CW];
+    int dst[CA + CW], grp[CA + CW];
+#pragma unroll
+    for (int i = 0; i < CA + CW; ++i) {
+        const int rows8 = i < CA ? TM / 8 : TN / 8;
+        const int q = min(wave + (i < CA ? i : i - CA) * W, KG * rows8 - 1);
+        grp[i] = q / rows8;
+        const int row = q % rows8 * 8 + (lane >> 3);
+        dst[i] = grp[i] * kPart + (i < CA ? 0 : TM * 128) + q % rows8 * 1024;
+        const uint32_t r = i < CA ? tile_row(row) : (uint32_t)min((int64_t)row, a.N - 1 - t.n0);
+        src[i] = r * (uint32_t)a.K + 16 * ((lane & 7) ^ (row >> 1 & 7));
+    }
+    // the scale copy that this wave issues in step c of a batch
+    auto part_of = [&](int c) __attribute__((always_inline)) { return min((c & (SB - 1)) * W + wave, TM / 8); };
+    auto issue_scale = [&](int b, int q, uint32_t row) __attribute__((always_inline)) {  // part q of batch b; row: from the table
+        const uint32_t at = row + 4 * min(8 * b + (lane & 7), nkb - 1);
+        buffer2lds4(q < TM / 8 ? rsa : rsw, lds + kBatches + b % 3 * kBatch + q * 256, at, 0);
+    };
+    // Lines fetched ahead into L2: the 32 tiles that an XCD runs at a time are four row tiles by eight column tiles, so each
+    // fetches an eighth of its A rows and a quarter of its weight rows, one 4-byte piece of every line, two steps before
+    // the copies need them.  Without it every step waits for the first reader's miss.
+    constexpr int kDistance = 2, kLines = (TM / 8 + TN / 4 + W - 1) / W;
+    const int line = wave * kLines + min(lane, kLines - 1);
+    const bool ahead_w = wave * kLines >= TM / 8;
+    const uint32_t ahead = (ahead_w ? (uint32_t)min((int64_t)(t.tm & 3) * (TN / 4) + min(line - TM / 8, TN / 4 - 1), a.N - 1 - t.n0)
+                                    : tile_row((t.tn & 7) * (TM / 8) + min(line, TM / 8 - 1))) * (uint32_t)a.K;
+    const uint8_t* ahead_base = ahead_w ? a.qw + (t.e * a.N + t.n0) * a.K : a.qa + arow0 * a.K;
+    const __amdgpu_buffer_rsrc_t rahead = __builtin_amdgcn_make_buffer_rsrc((void*)ahead_base, (short)0, -1, kRawWord3);
+    int ahead_at = min(kDistance * KG, nkb - 1) * 128;
+    // copy i of the C that go with step u, into its slot (blocks past the end: the last one again)
+    auto issue = [&](int u, int slot, int i, uint32_t row) __attribute__((always_inline)) {
+        if (i == 0) issue_scale(u / SB + 1, part_of(u), row);
+        else if (i == CA + CW + 1) {
+            buffer2lds4(rahead, lds + kSink, ahead, ahead_at);
+            ahead_at = min(ahead_at + KG * 128, (nkb - 1) * 128);
+        } else buffer2lds16(i <= CA ? ra : rw, lds + slot * kSlot + dst[i - 1], src[i - 1], min(u * KG + grp[i - 1], nkb - 1) * 128);
+    };
+
+    // LDS addresses: a per-lane base plus the slot and an immediate
+    const uint32_t base = lds_addr(lds);
+    const int key = l16 >> 1;
+    const uint32_t c0 = 16 * (g ^ key), c1 = 16 * ((g + 4) ^ key);
+    const uint32_t xrow = base + kg * kPart + (16 * FM * wm + l16) * 128, wrow = base + kg * kPart + TM * 128 + (16 * FN * wn + l16) * 128;
+    const uint32_t x0 = xrow + c0, x1 = xrow + c1, w0 = wrow + c0, w1 = wrow + c1;
+    const uint32_t xs = base + kBatches + 32 * (16 * FM * wm + l16);
+    // weight scales: fragment f is in block (n / 128) of its first column; the wave's fragments touch two at most
+    const int nw = (int)(t.n0 - nb0 * 128) + 16 * FN * wn;  // from the first block's start
+    const uint32_t ws = base + kBatches + 32 * (TM + nw / 128);
+    const int cut = 8 - nw % 128 / 16;  // fragments f < cut are in the first of the two
+    const uint32_t trow = base + kTable + 4 * (lane >> 3);
+
+    v4f acc[FN][FM] = {};
+    v4u wl[FN], wh[FN], xl[FM], xh[FM];
+    uint32_t sx[FM], sw[2], row[1];
+
+    __syncthreads();  // the table
+    for (int q = wave; q <= TM / 8; q += W) issue_scale(0, q, table[8 * q + (lane >> 3)]);
+    uint32_t first[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) first[s] = table[8 * part_of(s) + (lane >> 3)];
+    wait_vmcnt<0>();
+    static_for<S>([&](auto s) {
+        static_for<C>([&](auto i) {
+            if (s < S - 1 || i < kEarly) issue(s, s, i, first[s]);
+        });
+    });
+    auto scales_at = [&](int u) __attribute__((always_inline)) {  // offset of step u's scales (this group's block) in the batches
+        const int b = u * KG + kg;
+        return (uint32_t)((b >> 3) % 3 * kBatch + 4 * (b & 7));
+    };
+    wait_vmcnt<(S - 2) * C + kEarly>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<2>([&](auto i) {
+        sw[i] = lds_read4(scales_at(0) + ws + 32 * i);
+        wl[i] = lds_read16_at<i * 2048>(w0);
+        wh[i] = lds_read16_at<i * 2048>(w1);
+    });
+    static_for<FM>([&](auto j) {
+        sx[j] = lds_read4(scales_at(0) + xs + 512 * j);
+        xl[j] = lds_read16_at<j * 2048>(x0);
+        xh[j] = lds_read16_at<j * 2048>(x1);
+    });
+    row[0] = lds_read4(trow + 32 * part_of(S));
+    // ends a step: what is carried into the next one has arrived
+    auto arrive = [&]() __attribute__((always_inline)) {
+        lds_wait<0>();
+        asm volatile("" : "+v"(wl[0]), "+v"(wh[0]), "+v"(wl[1]), "+v"(wh[1]));
+        lds_tie(sx);
+        lds_tie(sw);
+        lds_tie(xl);
+        lds_tie(xh);
+        lds_tie(row);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    arrive();
+
+    // step u in slot s
+    auto step = [&](int u, auto sc) __attribute__((always_inline)) {
+        constexpr int s = decltype(sc)::value;
+        constexpr uint32_t at = s * kSlot, next = (s + 1) % S * kSlot;
+        float fx[FM];
+#pragma unroll
+        for (int j = 0; j < FM; ++j) fx[j] = KG == 1 || u * KG + kg < nkb ? __uint_as_float(sx[j]) : 0.f;
+        const float fw0 = __uint_as_float(__builtin_amdgcn_readfirstlane(sw[0])),
+                    fw1 = __uint_as_float(__builtin_amdgcn_readfirstlane(sw[1]));
+        if constexpr (kOneBlock) {
+#pragma unroll
+            for (int j = 0; j < FM; ++j) fx[j] *= fw0;
+        }
+        v4f p[3];
+        v4u nwl[2], nwh[2], nxl[kFree + 1], nxh[kFree + 1];
+        uint32_t nrow[1];
+        auto scale = [&](auto ic, int f, int j) __attribute__((always_inline)) {
+            const v4f v = p[decltype(ic)::value % 3];
+            const float m = kOneBlock ? fx[j] : fx[j] * (f < cut ? fw0 : fw1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[f][j][i] = __builtin_fmaf(v[i], m, acc[f][j][i]);
+        };
+        // MFMA i's fragments: weight-major, then the last two weight fragments row by row
+        auto fof = [](int i) constexpr { return i < kFirst ? i / FM : FN - 2 + (i - kFirst) % 2; };
+        auto jof = [](int i) constexpr { return i < kFirst ? i % FM : (i - kFirst) / 2; };
+        static_for<kMf>([&](auto ic) {
+            constexpr int i = decltype(ic)::value, f = fof(i), j = jof(i);
+            if constexpr (i < kFirst && j == 0) {  // fragment f's reads were issued two fragments ago
+                if constexpr (f >= 2) {
+                    lds_wait<2>();
+                    asm volatile("" : "+v"(wl[f]), "+v"(wh[f]));
+                }
+                wl[f + 2] = lds_read16_at<(f + 2) * 2048>(w0 + at);
+                wh[f + 2] = lds_read16_at<(f + 2) * 2048>(w1 + at);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (i == kFirst) {
+                if constexpr (FN > 2) {
+                    lds_wait<0>();
+                    if constexpr (FN > 3) asm volatile("" : "+v"(wl[FN - 2]), "+v"(wh[FN - 2]));
+                    asm volatile("" : "+v"(wl[FN - 1]), "+v"(wh[FN - 1]));
+                }
+                wait_vmcnt<(S - 2) * C + kAhead>();  // the line fetch is the last of a step's copies
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (kFirst == 0) static_for<C>([&](auto q) { issue(u + S, s, q, row[0]); });
+                const uint32_t sat = scales_at(u + 1);
+                static_for<2>([&](auto q) { sw[q] = lds_read4(sat + ws + 32 * q); });
+                static_for<FM>([&](auto q) { sx[q] = lds_read4(sat + xs + 512 * q); });
+                nrow[0] = lds_read4(trow + 32 * part_of(u + 1 + S));
+                static_for<2>([&](auto q) {
+                    nwl[q] = lds_read16_at<q * 2048>(w0 + next);
+                    nwh[q] = lds_read16_at<q * 2048>(w1 + next);
+                });
+                static_for<kFree>([&](auto q) {
+                    nxl[q] = lds_read16_at<(FM - kFree + q) * 2048>(x0 + next);
+                    nxh[q] = lds_read16_at<(FM - kFree + q) * 2048>(x1 + next);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            p[i % 3] = block_mfma(operand(wl[f], wh[f]), operand(xl[j], xh[j]));
+            __builtin_amdgcn_sched_barrier(0);  // the product two back is scaled behind this MFMA, not ahead of it
+            if constexpr (i >= 2) scale(std::integral_constant<int, i - 2>{}, fof(i - 2), jof(i - 2));
+            // copies: the slot of the step before, then this step's
+            if constexpr (i < kSpan)
+                static_for<(i + 1) * kLate / kSpan - i * kLate / kSpan>(
+                    [&](auto q) { issue(u - 1 + S, (s + S - 1) % S, kEarly + i * kLate / kSpan + q, 0); });
+            if constexpr (i >= kFirst && kFirst > 0) {
+                constexpr int k = i - kFirst;
+                static_for<(k + 1) * kEarly / (2 * FM) - k * kEarly / (2 * FM)>(
+                    [&](auto q) { issue(u + S, s, k * kEarly / (2 * FM) + q, row[0]); });
+            }
+            // row fragment j is free one MFMA after its last use
+            if constexpr (i > kFirst + 1 && (i - kFirst) % 2 == 0 && (i - kFirst) / 2 - 1 < FM - kFree) {
+                constexpr int q = (i - kFirst) / 2 - 1;
+                xl[q] = lds_read16_at<q * 2048>(x0 + next);
+                xh[q] = lds_read16_at<q * 2048>(x1 + next);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        scale(std::integral_constant<int, kMf - 2>{}, fof(kMf - 2), jof(kMf - 2));
+        if constexpr (kFree == 0) {
+            xl[FM - 1] = lds_read16_at<(FM - 1) * 2048>(x0 + next);
+            xh[FM - 1] = lds_read16_at<(FM - 1) * 2048>(x1 + next);
+        }
+        scale(std::integral_constant<int, kMf - 1>{}, fof(kMf - 1), jof(kMf - 1));
+        __builtin_amdgcn_sched_barrier(0);
+        lds_wait<0>();
+        asm volatile("" : "+v"(nwl[0]), "+v"(nwh[0]), "+v"(nwl[1]), "+v"(nwh[1]));
+        lds_tie(nrow);
+        wl[0] = nwl[0], wh[0] = nwh[0], wl[1] = nwl[1], wh[1] = nwh[1], row[0] = nrow[0];
+#pragma unroll
+        for (int q = 0; q < kFree; ++q) {
+            asm volatile("" : "+v"(nxl[q]), "+v"(nxh[q]));
+            xl[FM - kFree + q] = nxl[q], xh[FM - kFree + q] = nxh[q];
+        }
+        arrive();
+    };
+    for (int u = 0; u < steps; u += S)
+        static_for<S>([&](auto s) {
+            if (u + s < steps) step(u + s, s);
+        });
+    wait_vmcnt<0>();  // the copies past the end still write to LDS
+
+    if constexpr (KG > 1) {  // the groups' sums through LDS, in group order
+        __syncthreads();
+        v4f* red = reinterpret_cast<v4f*>(lds) + (wm * WN + wn) * FN * FM * 64 + lane;
+        constexpr int kGroup = WM * WN * FN * FM * 64;
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < FN * FM; ++i) red[(kg - 1) * kGroup + i * 64] = acc[i / FM][i % FM];
+        }
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll
+        for (int q = 0; q < KG - 1; ++q)
+#pragma unroll
+            for (int i = 0; i < FN * FM; ++i) acc[i / FM][i % FM] += red[q * kGroup + i * 64];
+    }
+    const bool vec = a.N % 4 == 0 && ((uintptr_t)a.y & 7) == 0;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        const int64_t m = t.m0 + 16 * (FM * wm + j) + l16;
+        if (m >= t.r1) continue;
+        const bool ok = a_row(a, m) >= 0;
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+            const v4f zero = {0.f, 0.f, 0.f, 0.f};
+            store4(a.y + m * a.N, a.N, t.n0 + 16 * (FN * wn + f) + 4 * g, ok ? acc[f][j] : zero, vec);
+        }
+    }
+}
+
+}  // namespace b128
+}  // namespace mx
