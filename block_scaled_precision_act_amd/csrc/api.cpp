@@ -243,6 +243,25 @@ MX_API mx_status gemm_a8w8_b128_bf16(const void* qa, const float* sa, const void
     return launched(mx::launch_gemm_b128(qa, sa, qw, sw, y_bf16, M, N, K, reinterpret_cast<hipStream_t>(stream)));
 }
 
+MX_API size_t linear_a8w8_b128_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (check_gemm_b128(M, N, K) != MX_SUCCESS || M == 0 || N == 0) return 0;
+    return mx::linear_b128_workspace_bytes(M, N, K);
+}
+
+MX_API mx_status linear_a8w8_b128_bf16(const void* x_bf16, const void* qw, const float* sw, void* y_bf16, int64_t M,
+                                       int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+    mx_status st = check_gemm_b128(M, N, K);
+    if (st != MX_SUCCESS) return st;
+    if (M == 0 || N == 0) return MX_SUCCESS;
+    if (!x_bf16 || !qw || !sw || !y_bf16) return MX_ERROR_INVALID_VALUE;
+    const size_t need = mx::linear_b128_workspace_bytes(M, N, K);
+    if (workspace_bytes < need || (need && !workspace)) return MX_ERROR_WORKSPACE;
+    if (!aligned(x_bf16, 16) || !aligned(qw, 16) || !aligned(sw, 4) || !aligned(y_bf16, 2) || (need && !aligned(workspace, 16)))
+        return MX_ERROR_MISALIGNED;
+    if ((st = check_device()) != MX_SUCCESS) return st;
+    return launched(mx::launch_linear_b128(x_bf16, qw, sw, y_bf16, M, N, K, workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
 MX_API mx_status gemm_a8w8_b128_grouped_bf16(const void* qa, const float* sa, int64_t a_rows, const void* qw,
                                              const float* sw, void* y_bf16, const int32_t* offsets, const int32_t* rows,
                                              int64_t G, int64_t T, int64_t N, int64_t K, void* stream) {

@@ -70,6 +70,17 @@ hipError_t launch_gemm_b128(const void* qa, const float* sa, const void* qw, con
                    reinterpret_cast<uint16_t*>(y), nullptr, nullptr, M, M, N, K, 1}, st);
 }
 
+// codes [M, K], then scales [M, K / 128]
+size_t linear_b128_workspace_bytes(int64_t M, int64_t, int64_t K) { return (size_t)M * K + (size_t)M * (K / 128) * 4; }
+
+hipError_t launch_linear_b128(const void* x, const void* qw, const float* sw, void* y, int64_t M, int64_t N, int64_t K,
+                              void* workspace, hipStream_t st) {
+    uint8_t* q = reinterpret_cast<uint8_t*>(workspace);
+    float* s = reinterpret_cast<float*>(q + M * K);
+    const hipError_t err = launch_quant_b128_act(x, M, K, q, s, st);
+    return err != hipSuccess ? err : launch_gemm_b128(q, s, qw, sw, y, M, N, K, st);
+}
+
 hipError_t launch_gemm_b128_grouped(const void* qa, const float* sa, int64_t arows, const void* qw, const float* sw,
                                     void* y, const int32_t* offsets, const int32_t* rows, int64_t G, int64_t M, int64_t N,
                                     int64_t K, hipStream_t st) {

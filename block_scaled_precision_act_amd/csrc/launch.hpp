@@ -41,6 +41,9 @@ hipError_t launch_quant_b128_act(const void* x, int64_t M, int64_t K, void* q, f
 hipError_t launch_quant_b128_weight(const float* w, int64_t N, int64_t K, void* q, float* s, hipStream_t st);
 hipError_t launch_gemm_b128(const void* qa, const float* sa, const void* qw, const float* sw, void* y, int64_t M, int64_t N,
                             int64_t K, hipStream_t st);
+hipError_t launch_linear_b128(const void* x, const void* qw, const float* sw, void* y, int64_t M, int64_t N, int64_t K,
+                              void* workspace, hipStream_t st);
+size_t linear_b128_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_b128_grouped(const void* qa, const float* sa, int64_t arows, const void* qw, const float* sw,
                                     void* y, const int32_t* offsets, const int32_t* rows, int64_t G, int64_t M, int64_t N,
                                     int64_t K, hipStream_t st);

@@ -6,7 +6,9 @@
 // Every step is integer arithmetic whose result does not depend on the order of the atomic additions.
 //   Up to kOneMax choices one workgroup does it all in LDS, in one launch.  Above, one kernel counts the
 // experts of every chunk of choices and a second one, a workgroup per chunk, sums the counts of the chunks
-// before its own (all counts are read by every workgroup: chunks * E integers, from L2) and places its chunk.
+// before its own and places its chunk.  Every workgroup reads all counts (chunks * E integers, from L2), all its
+// threads sharing them out by expert and chunk: with a few threads walking the chunks one after another, 131072
+// choices over 256 experts took 51 us.
 //
 // Balance loss.  p = softmax(logits[t]) over the experts, f_e = counts_e / sum(counts), n the tokens whose
 // mask is not 0: loss = coef * E * sum_e f_e * mean_t p_te = sum_t sum_e w_e p_te with w_e = coef E f_e / n, so
@@ -21,7 +23,7 @@ namespace {
 
 constexpr int kMaxE = 1024;
 constexpr int kOneThreads = 1024, kOneMax = 8192;
-constexpr int kThreads = 256, kChunk = 2048;  // choices per workgroup of the two-kernel form
+constexpr int kThreads = 512, kChunk = 2048;  // choices per workgroup of the two-kernel form
 
 __device__ __forceinline__ int id_at(const void* ids, bool wide, int64_t i, int E) {
     if (wide) {
@@ -157,44 +159,51 @@ __global__ __launch_bounds__(kThreads) void moe_route_place(const void* ids, boo
                                                             const int* __restrict__ hist, int32_t* counts, int32_t* offsets,
                                                             int32_t* rows, int32_t* slots) {
     constexpr int W = kThreads / 64, PER = kMaxE / kThreads;
-    __shared__ int h[W * kMaxE];
+    __shared__ int h[W * kMaxE], all[kMaxE], before[kMaxE];
     __shared__ int tmp[W];
     const int chunk = blockIdx.x, chunks = gridDim.x;
     for (int i = threadIdx.x; i < W * E; i += kThreads) h[i] = 0;
+    for (int e = threadIdx.x; e < E; e += kThreads) all[e] = before[e] = 0;
     __syncthreads();
     const int64_t c0 = (int64_t)chunk * kChunk, c1 = min(c0 + kChunk, n);
     const Chunk<W> c(ids, wide, E, c0, c1);
     c.count(h);
-    // thread t: experts PER t .. PER t + PER - 1
-    int all[PER] = {}, before[PER] = {}, sum = 0;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int e = PER * threadIdx.x + k;
-        if (e >= E) continue;
-        for (int b = 0; b < chunks; ++b) {
+    // the counts of all chunks: thread t takes expert t % span of chunks t / span, t / span + parts, ...
+    const int bits = c.bits < 9 ? c.bits : 9, span = 1 << bits, parts = kThreads >> bits;  // kThreads = 512
+    for (int e = threadIdx.x & (span - 1); e < E; e += span) {
+        int sum = 0, low = 0;
+#pragma unroll 8
+        for (int b = threadIdx.x >> bits; b < chunks; b += parts) {
             const int v = hist[(int64_t)b * E + e];
-            all[k] += v;
-            before[k] += b < chunk ? v : 0;
+            sum += v;
+            low += b < chunk ? v : 0;
         }
-        sum += all[k];
+        atomicAdd(all + e, sum);
+        atomicAdd(before + e, low);
     }
+    __syncthreads();
+    // thread t: experts PER t .. PER t + PER - 1
+    int sum = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) sum += PER * (int)threadIdx.x + k < E ? all[PER * threadIdx.x + k] : 0;
     int total;
-    int start = block_scan<kThreads>(sum, tmp, total);  // its barriers also end the counting above
+    int start = block_scan<kThreads>(sum, tmp, total);
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int e = PER * threadIdx.x + k;
         if (e >= E) continue;
         if (chunk == 0) {
-            counts[e] = all[k];
+            counts[e] = all[e];
             offsets[e] = start;
         }
-        int p = start + before[k];
+        int p = start + before[e];
+#pragma unroll
         for (int w = 0; w < W; ++w) {
             const int v = h[w * E + e];
             h[w * E + e] = p;
             p += v;
         }
-        start += all[k];
+        start += all[e];
     }
     if (chunk == 0 && threadIdx.x == 0) offsets[E] = total;
     __syncthreads();
@@ -208,18 +217,35 @@ __global__ __launch_bounds__(kThreads) void moe_route_place(const void* ids, boo
 // ---------------------------------------------------------------- balance loss
 constexpr int kLossThreads = 512, kLossBlocks = 512;
 
-// Sums and maxima over the L lanes that hold a row (L a power of two; every lane of them active)
-template <int L>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < L; d <<= 1) v += __shfl_xor(v, d);
+// Sums and maxima over the L lanes that hold a row (L = 8, 16, 32 or 64; every lane of them active), without LDS: lane
+// swaps within 16 lanes by DPP, then rows of 16 and halves of the wave exchanged.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int L, typename F>
+__device__ __forceinline__ float row_reduce(float v, F&& f) {
+    v = f(v, dpp<0xB1>(v));   // quad_perm [1,0,3,2]
+    v = f(v, dpp<0x4E>(v));   // quad_perm [2,3,0,1]
+    v = f(v, dpp<0x141>(v));  // row_half_mirror
+    if constexpr (L >= 16) v = f(v, dpp<0x140>(v));  // row_mirror
+    if constexpr (L >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    if constexpr (L >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
     return v;
 }
 template <int L>
+__device__ __forceinline__ float row_sum(float v) {
+    return row_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
 __device__ __forceinline__ float row_max(float v) {
-#pragma unroll
-    for (int d = 1; d < L; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    return row_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // Row t's softmax: lane j of L holds experts j, j + L, ...  A row with no logit above -infinity has no
@@ -278,7 +304,18 @@ __global__ __launch_bounds__(kLossThreads) void moe_balance_kernel(const void* _
     for (int e = threadIdx.x; e < E; e += kLossThreads) chosen += counts[e];
     chosen = block_sum<int64_t, kLossThreads>(chosen, tmp);
     if (mask) {
-        for (int64_t t = threadIdx.x; t < T; t += kLossThreads) live += mask[t] != 0;
+        // 16 bytes at a time from the first aligned one; every workgroup counts them all
+        const int64_t head = min((int64_t)(-(uintptr_t)mask & 15), T), vecs = (T - head) / 16;
+        const uint4* v = reinterpret_cast<const uint4*>(mask + head);
+        for (int64_t i = threadIdx.x; i < vecs; i += kLossThreads) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int b = 0; b < 32; b += 8) live += (w[k] >> b & 0xff) != 0;
+        }
+        for (int64_t t = threadIdx.x; t < head; t += kLossThreads) live += mask[t] != 0;
+        for (int64_t t = head + 16 * vecs + threadIdx.x; t < T; t += kLossThreads) live += mask[t] != 0;
         live = block_sum<int64_t, kLossThreads>(live, tmp);
     } else {
         live = T;
@@ -362,10 +399,11 @@ hipError_t by_width(int64_t E, F&& f) {
     if (E <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
     return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
+int64_t lanes_of(int64_t E) { return E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64; }
+// One workgroup, and so one launch, up to eight rounds of it; a second launch costs about as much.
 int64_t loss_blocks(int64_t T, int64_t E) {
-    const int64_t lanes = E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64;
-    const int64_t b = (T * lanes + kLossThreads - 1) / kLossThreads;
-    return b < kLossBlocks ? b : kLossBlocks;
+    const int64_t b = (T * lanes_of(E) + kLossThreads - 1) / kLossThreads;
+    return b <= 8 ? 1 : b < kLossBlocks ? b : kLossBlocks;
 }
 
 }  // namespace
@@ -417,8 +455,7 @@ hipError_t launch_moe_balance(const void* logits, bool half, int64_t T, int64_t 
 
 hipError_t launch_moe_balance_grad(const void* logits, bool half, int64_t T, int64_t E, const float* w, const uint8_t* mask,
                                    const float* grad_loss, void* dlogits, hipStream_t st) {
-    const int64_t lanes = E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64;
-    const int64_t blocks = (T * lanes + kLossThreads - 1) / kLossThreads;
+    const int64_t blocks = (T * lanes_of(E) + kLossThreads - 1) / kLossThreads;
     return by_width(E, [&](auto l, auto v) {
         constexpr int L = decltype(l)::value, V = decltype(v)::value;
         const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096)), block(kLossThreads);

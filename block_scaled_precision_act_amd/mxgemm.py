@@ -79,12 +79,15 @@ def lib() -> ctypes.CDLL:
                 ("b128_quant_act_fp8", [vp, i64, i64, vp, vp, vp]),
                 ("b128_quant_weight_f32", [vp, i64, i64, vp, vp, vp]),
                 ("gemm_a8w8_b128_bf16", [vp, vp, vp, vp, vp, i64, i64, i64, vp]),
+                ("linear_a8w8_b128_bf16", [vp, vp, vp, vp, i64, i64, i64, vp, sz, vp]),
                 ("gemm_a8w8_b128_grouped_bf16", [vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp]),
                 ("moe_route", [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, sz, vp]),
                 ("moe_balance_loss", [vp, i32, i64, i64, vp, vp, f32, vp, vp, vp, sz, vp]),
                 ("moe_balance_loss_grad", [vp, i32, i64, i64, vp, vp, vp, vp, vp])):
             getattr(L, name).argtypes = args
             getattr(L, name).restype = i32
+        L.linear_a8w8_b128_workspace_bytes.argtypes = [i64, i64, i64]
+        L.linear_a8w8_b128_workspace_bytes.restype = sz
         L.moe_route_workspace_bytes.argtypes = [i64, i64, i64]
         L.moe_route_workspace_bytes.restype = sz
         L.moe_balance_loss_workspace_bytes.argtypes = [i64, i64]
@@ -160,6 +163,14 @@ def b128_quant_weight_f32(w, N, K, q, s, stream=None) -> int:
 
 def gemm_a8w8_b128_bf16(qa, sa, qw, sw, y, M, N, K, stream=None) -> int:
     return lib().gemm_a8w8_b128_bf16(qa, sa, qw, sw, y, M, N, K, stream)
+
+
+def linear_a8w8_b128_workspace_bytes(M, N, K) -> int:
+    return lib().linear_a8w8_b128_workspace_bytes(M, N, K)
+
+
+def linear_a8w8_b128_bf16(x, qw, sw, y, M, N, K, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return lib().linear_a8w8_b128_bf16(x, qw, sw, y, M, N, K, workspace, workspace_bytes, stream)
 
 
 def gemm_a8w8_b128_grouped_bf16(qa, sa, a_rows, qw, sw, y, offsets, rows, G, T, N, K, stream=None) -> int:
@@ -363,16 +374,25 @@ def linear_a8w8(x, qw, sw):
 # ------------------------------------------------------------------ block-128 FP8
 def _raw_stream(device):
     """The current stream's handle on `device`, which must be the current device: the library launches there."""
-    torch = _torch()
-    if device.index != torch.cuda.current_device():
-        raise ValueError("operands are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
-    return torch.cuda.current_stream().cuda_stream
+    cuda = _torch().cuda
+    index = cuda.current_device()
+    if device.index != index:
+        raise ValueError("operands are on %s, the current device is cuda:%d" % (device, index))
+    # the handle itself: building torch's Stream object around it costs as much as a kernel launch
+    return _torch()._C._cuda_getCurrentRawStream(index)
 
 
 def _same_device(like, **others):
+    device = like.device
     for name, t in others.items():
-        if t is not None and t.device != like.device:
-            raise ValueError("%s must be on %s, got %s" % (name, like.device, t.device))
+        if t is not None and t.device != device:
+            raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+
+
+def _scratch(nbytes, device):
+    """Memory for one call, from torch's allocator, which keeps it apart from calls on other streams and in
+    captured graphs."""
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device) if nbytes else None
 
 
 def quant_act_b128(x, q=None, s=None):
@@ -418,10 +438,24 @@ def gemm_a8w8_b128(qa, sa, qw, sw, y=None):
     return y
 
 
-def linear_a8w8_b128(x, qw, sw):
-    """The block-128 FP8 layer: dynamic quantization of BF16 x (one scale per 128 values), then the GEMM."""
-    qa, sa = quant_act_b128(x)
-    return gemm_a8w8_b128(qa, sa, qw, sw)
+def linear_a8w8_b128(x, qw, sw, y=None):
+    """The block-128 FP8 layer through linear_a8w8_b128_bf16: BF16 x [M, K], quantized dynamically (one scale per 128
+    values) -> BF16 Y [M, N]."""
+    torch = _torch()
+    _need(x, torch.bfloat16, 2, "x")
+    _need(qw, torch.uint8, 2, "qw")
+    _need(sw, torch.float32, 2, "sw")
+    M, K = x.shape
+    N = qw.shape[0]
+    if qw.shape[1] != K or sw.shape != ((N + 127) // 128, K // 128):
+        raise ValueError("inconsistent block-128 A8W8 layer shapes")
+    _same_device(x, qw=qw, sw=sw)
+    y = _out(y, torch.bfloat16, (M, N), x, "y")
+    need = lib().linear_a8w8_b128_workspace_bytes(M, N, K)
+    ws = _scratch(need, x.device)
+    _ok(lib().linear_a8w8_b128_bf16(x.data_ptr(), qw.data_ptr(), sw.data_ptr(), y.data_ptr(), M, N, K,
+                                    ws.data_ptr() if need else None, need, _raw_stream(x.device)), "linear_a8w8_b128_bf16")
+    return y
 
 
 def gemm_a8w8_b128_grouped(qa, sa, qw, sw, offsets, rows=None, y=None):
@@ -461,12 +495,6 @@ def moe_balance_loss_workspace_bytes(T, E) -> int:
     return lib().moe_balance_loss_workspace_bytes(T, E)
 
 
-def _scratch(nbytes, device):
-    """Memory for one call, from torch's allocator, which keeps it apart from calls on other streams and in
-    captured graphs."""
-    return _torch().empty(nbytes, dtype=_torch().uint8, device=device) if nbytes else None
-
-
 def moe_route(ids, experts):
     """Expert ids int32 or int64 [T, top] (a value outside 0 .. experts - 1 is no choice) -> int32 counts [E],
     offsets [E + 1], rows [T * top] (the token of every packed row, -1 behind the last) and slots [T, top] (the
@@ -476,10 +504,12 @@ def moe_route(ids, experts):
         raise TypeError("ids must be an int32 or int64 torch.Tensor")
     _need(ids, ids.dtype, 2, "ids")
     T, top = ids.shape
-    counts = torch.empty(experts, dtype=torch.int32, device=ids.device)
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
-    rows = torch.empty(T * top, dtype=torch.int32, device=ids.device)
-    slots = torch.empty((T, top), dtype=torch.int32, device=ids.device)
+    if experts < 1:
+        raise ValueError("experts must be positive")
+    n = T * top  # one allocation: four would cost more than the kernel
+    counts, offsets, rows, slots = torch.empty(2 * experts + 1 + 2 * n, dtype=torch.int32, device=ids.device).split_with_sizes(
+        (experts, experts + 1, n, n))
+    slots = slots.view(T, top)
     need = lib().moe_route_workspace_bytes(T, top, experts)
     ws = _scratch(need, ids.device)
     _ok(lib().moe_route(ids.data_ptr(), ids.element_size(), T, top, experts, counts.data_ptr(), offsets.data_ptr(),
@@ -514,8 +544,7 @@ def moe_balance_loss(logits, counts, coef, mask=None):
     if counts.shape[0] != E:
         raise ValueError("counts must have one entry per expert")
     _same_device(logits, counts=counts)
-    loss = torch.empty(1, dtype=torch.float32, device=logits.device)
-    weights = torch.empty(E, dtype=torch.float32, device=logits.device)
+    loss, weights = torch.empty(1 + E, dtype=torch.float32, device=logits.device).split_with_sizes((1, E))
     need = lib().moe_balance_loss_workspace_bytes(T, E)
     ws = _scratch(need, logits.device)
     _ok(lib().moe_balance_loss(logits.data_ptr(), dtype, T, E, counts.data_ptr(),

@@ -310,6 +310,18 @@ mx_status gemm_a8w8_b128_bf16(const void *qa, const float *sa, const void *qw, c
                               void *y_bf16, int64_t M, int64_t N, int64_t K, void *stream);
 
 /*
+ * The block-128 layer in one call: Y = the GEMM above on b128_quant_act_fp8(X).
+ *   x_bf16 [M, K] in (16-byte aligned); qw, sw, y_bf16, M, N, K as there;
+ *   workspace: linear_a8w8_b128_workspace_bytes(M, N, K) bytes, 16-byte aligned, any
+ *   content before and after (NULL when that is 0); calls that may overlap need
+ *   workspaces of their own.
+ */
+size_t linear_a8w8_b128_workspace_bytes(int64_t M, int64_t N, int64_t K);
+mx_status linear_a8w8_b128_bf16(const void *x_bf16, const void *qw, const float *sw, void *y_bf16,
+                                int64_t M, int64_t N, int64_t K,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Grouped block-128 A8W8 GEMM over MoE experts: rows offsets[e] ..
  * offsets[e+1]-1 of Y are products with expert weight e.
  *   qa [a_rows, K], sa [a_rows, K/128]; qw [G, N, K], sw [G, ceil(N/128), K/128];

@@ -38,12 +38,32 @@ def test_gemm(mx):
     assert f(*five, 4, -1, 128) == mx.MX_ERROR_INVALID_VALUE
     assert f(*five, 4, 4, 64) == mx.MX_ERROR_UNSUPPORTED_SHAPE
     assert f(*five, 1 << 32, 4, 128) == mx.MX_ERROR_UNSUPPORTED_SHAPE
+    assert f(*five, 4, 4, 1 << 23) == mx.MX_ERROR_UNSUPPORTED_SHAPE           # a tile's rows past 32-bit offsets
+    assert f(*five, 1 << 30, 1 << 30, 128) == mx.MX_ERROR_UNSUPPORTED_SHAPE   # more tiles than a grid holds
     for i in range(5):
         assert f(*(None if j == i else FAKE for j in range(5)), 4, 4, 128) == mx.MX_ERROR_INVALID_VALUE
     for i, off in enumerate((8, 2, 8, 2, 1)):
         assert f(*(FAKE + (off if j == i else 0) for j in range(5)), 4, 4, 128) == mx.MX_ERROR_MISALIGNED
     assert f(*(None,) * 5, 0, 4, 128) == mx.MX_SUCCESS
     assert f(*(None,) * 5, 4, 0, 128) == mx.MX_SUCCESS
+
+
+def test_layer(mx):
+    f = mx.linear_a8w8_b128_bf16
+    need = mx.linear_a8w8_b128_workspace_bytes(40, 64, 256)
+    assert need > 0 and mx.linear_a8w8_b128_workspace_bytes(0, 64, 256) == 0 and mx.linear_a8w8_b128_workspace_bytes(4, 4, 100) == 0
+    four = (FAKE,) * 4
+    assert f(*four, -1, 64, 256) == mx.MX_ERROR_INVALID_VALUE
+    assert f(*four, 40, 64, 200) == mx.MX_ERROR_UNSUPPORTED_SHAPE
+    assert f(*four, 40, 64, 1 << 23, FAKE, 1 << 40) == mx.MX_ERROR_UNSUPPORTED_SHAPE
+    for i in range(4):
+        assert f(*(None if j == i else FAKE for j in range(4)), 40, 64, 256, FAKE, need) == mx.MX_ERROR_INVALID_VALUE
+    for i, off in enumerate((8, 8, 2, 1)):
+        assert f(*(FAKE + (off if j == i else 0) for j in range(4)), 40, 64, 256, FAKE, need) == mx.MX_ERROR_MISALIGNED
+    assert f(*four, 40, 64, 256) == mx.MX_ERROR_WORKSPACE
+    assert f(*four, 40, 64, 256, FAKE, need - 1) == mx.MX_ERROR_WORKSPACE
+    assert f(*four, 40, 64, 256, FAKE + 8, need) == mx.MX_ERROR_MISALIGNED
+    assert f(*(None,) * 4, 0, 64, 256) == mx.MX_SUCCESS
 
 
 def test_grouped_gemm(mx):
@@ -54,6 +74,7 @@ def test_grouped_gemm(mx):
     assert f(FAKE, FAKE, 4, FAKE, FAKE, FAKE, FAKE, None, 2, 4, 16, 96) == mx.MX_ERROR_UNSUPPORTED_SHAPE
     assert f(FAKE, FAKE, 3, FAKE, FAKE, FAKE, FAKE, None, 2, 4, 16, 128) == mx.MX_ERROR_INVALID_VALUE  # fewer rows than Y
     assert f(FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, 2, 4, 16, 128) == mx.MX_ERROR_INVALID_VALUE  # no row to gather
+    assert f(FAKE, FAKE, 1 << 25, FAKE, FAKE, FAKE, FAKE, FAKE, 2, 4, 16, 128) == mx.MX_ERROR_UNSUPPORTED_SHAPE  # 32-bit offsets
     for i in range(6):
         p = [None if j == i else FAKE for j in range(6)]
         assert f(p[0], p[1], 4, p[2], p[3], p[4], p[5], None, 2, 4, 16, 128) == mx.MX_ERROR_INVALID_VALUE
