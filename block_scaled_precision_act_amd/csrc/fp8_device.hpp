@@ -43,4 +43,40 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return max(max(a, b), max(c, d));
 }
 
+// scale of a block from its largest magnitude bit pattern
+__device__ __forceinline__ float block_scale(uint32_t mag_max) {
+    if (mag_max >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+    const float s = __uint_as_float(mag_max) / 448.0f;
+    return s == 0.0f ? 1.0f : s;
+}
+__device__ __forceinline__ float clamped_quotient(float x, float s) {
+    return __builtin_amdgcn_fmed3f(x / s, -448.0f, 448.0f);
+}
+
+// One block of 128 BF16 values held by 16 lanes, eight each: this lane's eight codes, and the block's scale.
+__device__ __forceinline__ uint2 quant_block_bf16x8(uint4 r, float& sc) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    uint32_t mag = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mag = max(mag, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+    mag = row16_max(mag);
+    sc = block_scale(mag);
+    if (mag >= 0x7f800000u) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    if (sc >= 0x1p-90f) {
+        const float rc = 1.0f / sc;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = div_corrected(v[i], sc, rc);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = clamped_quotient(v[i], sc);
+    }
+    return make_uint2(e4m3fn_x4(v[0], v[1], v[2], v[3]), e4m3fn_x4(v[4], v[5], v[6], v[7]));
+}
+
 }  // namespace mx

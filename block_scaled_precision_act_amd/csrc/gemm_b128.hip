@@ -1,11 +1,17 @@
 // gemm_b128.hip - entries of the A8W8 GEMM with one FP32 scale per block of 128 (kernels: gemm_b128.hpp).
 //
-// Which kernel.  A dense product of at most kRows rows streams the weight to registers (rows_kernel).  Anything else
-// takes the tile whose rounds over the CUs are estimated cheapest: time = rounds x the time of one round of that tile,
-// rounds = ceil(tiles / CUs).  One round of each tile, measured at K = 8192 and N = 7168 (us, launch taken off):
-//   32 x 64 14.5, 64 x 64 17.5, 64 x 128 29, 128 x 128 40, 256 x 128 70, 256 x 256 115
-// so a small product fills the CUs with small tiles and a large one is read least by large tiles.  Grouped products
-// count their row tiles from the mean group.
+// Dense products take the tile whose rounds over the CUs are estimated cheapest: rounds = ceil(tiles / CUs), times the time
+// of one round of that tile (kTiles; measured at K = 8192 and N = 7168, us, launch taken off), so a small product fills the
+// CUs with small tiles and a large one is read least by large tiles.
+//
+// Grouped products stream the experts' weights, so a tile should hold a whole group: by the mean group's rows, with
+// steps down while the tiles would leave half of the CUs idle.  Measured with 32 experts of [2048, 7168], us:
+//   rows        2     8    16    32    64   128   256   512
+//   16 x 64    91   105   115
+//   32 x 128   98    98    98   123   171
+//   64 x 128        104   103   109   142   195   315
+//   128 x 128                   121   134   173   260   419
+//   256 x 256                               221   237   347
 #include "gemm_b128.hpp"
 #include "launch.hpp"
 
@@ -14,12 +20,15 @@ namespace {
 
 using b128::Args;
 
-constexpr int64_t kRows = 8;
-
-hipError_t launch_rows(const Args& a, hipStream_t st) {
-    hipLaunchKernelGGL((b128::rows_kernel<1, 1, 8, 3>), dim3((unsigned)((a.N + 15) / 16)), dim3(512), 0, st, a);
+// The layer in one launch, for rows that the GEMM quantizes itself (see quant_rows_kernel).
+constexpr int64_t kQuantRows = 2, kQuantLds = 32 * 1024;
+constexpr int kQuantWaves = 16;
+hipError_t launch_quant_rows(const Args& a, hipStream_t st) {
+    hipLaunchKernelGGL((b128::quant_rows_kernel<kQuantWaves, 2>), dim3((unsigned)((a.N + 15) / 16)), dim3(64 * kQuantWaves),
+                       (unsigned)b128::quant_lds_bytes(a.M, a.K, kQuantWaves), st, a);
     return hipGetLastError();
 }
+bool one_launch(int64_t M, int64_t K) { return M <= kQuantRows && b128::quant_lds_bytes(M, K, kQuantWaves) <= kQuantLds; }
 
 template <int FM, int FN, int WM, int WN, int KG, int S>
 hipError_t launch_tile(const Args& a, hipStream_t st) {
@@ -38,22 +47,31 @@ struct Tile {
     hipError_t (*launch)(const Args&, hipStream_t);
 };
 const Tile kTiles[] = {
-    {32, 64, 14.5, launch_tile<2, 2, 1, 2, 2, 4>},   {64, 64, 17.5, launch_tile<2, 4, 2, 1, 2, 4>},
-    {64, 128, 29.0, launch_tile<2, 4, 2, 2, 2, 2>},  {128, 128, 40.0, launch_tile<2, 4, 4, 2, 1, 3>},
-    {256, 128, 70.0, launch_tile<4, 4, 4, 2, 1, 2>}, {256, 256, 115.0, launch_tile<4, 8, 4, 2, 1, 2>},
+    {16, 32, 10.2, launch_tile<1, 2, 1, 1, 4, 4>},   {16, 64, 10.8, launch_tile<1, 4, 1, 1, 4, 3>},
+    {32, 64, 12.8, launch_tile<2, 4, 1, 1, 4, 3>},   {64, 64, 17.4, launch_tile<2, 4, 2, 1, 2, 4>},
+    {64, 128, 29.5, launch_tile<2, 4, 2, 2, 1, 4>},  {128, 128, 40.5, launch_tile<2, 4, 4, 2, 1, 3>},
+    {256, 128, 70.0, launch_tile<4, 4, 4, 2, 1, 2>}, {256, 256, 113.0, launch_tile<4, 8, 4, 2, 1, 2>},
+};
+// for groups of up to `rows` rows in the mean
+struct GroupTile {
+    double rows;
+    int m, n;
+    hipError_t (*launch)(const Args&, hipStream_t);
+};
+const GroupTile kGroupTiles[] = {
+    {6, 16, 64, launch_tile<1, 4, 1, 1, 4, 3>},     {24, 32, 128, launch_tile<2, 4, 1, 2, 2, 3>},
+    {48, 64, 128, launch_tile<2, 4, 2, 2, 1, 4>},   {192, 128, 128, launch_tile<2, 4, 4, 2, 1, 3>},
+    {1e30, 256, 256, launch_tile<4, 8, 4, 2, 1, 2>},
 };
 
+int cus() { return device_cus() > 0 ? device_cus() : 256; }
+
 hipError_t launch(const Args& a, hipStream_t st) {
-    if (!a.offsets && a.M <= kRows) return launch_rows(a, st);
-    const double cus = device_cus() > 0 ? device_cus() : 256;
-    const double groups = a.offsets ? (double)(a.G < a.M ? a.G : a.M) : 1.0;
     const Tile* best = nullptr;
     double least = 0;
     for (const Tile& t : kTiles) {
-        const double tn = (double)((a.N + t.n - 1) / t.n), mean = (double)a.M / groups;
-        const double tm = a.offsets ? groups * (mean > 0.5 * t.m ? mean / t.m + 0.5 : 1.0) : (double)((a.M + t.m - 1) / t.m);
-        const double rounds = a.offsets ? (tm * tn > cus ? tm * tn / cus : 1.0) : (double)(int64_t)((tm * tn + cus - 1) / cus);
-        const double time = rounds * t.round;
+        const int64_t tiles = ((a.M + t.m - 1) / t.m) * ((a.N + t.n - 1) / t.n);
+        const double time = (double)((tiles + cus() - 1) / cus()) * t.round;
         if (!best || time < least) {
             best = &t;
             least = time;
@@ -62,19 +80,35 @@ hipError_t launch(const Args& a, hipStream_t st) {
     return best->launch(a, st);
 }
 
+hipError_t launch_grouped(const Args& a, hipStream_t st) {
+    const double groups = (double)(a.G < a.M ? a.G : a.M), rows = (double)a.M / groups;
+    const GroupTile* t = kGroupTiles;
+    while (rows > t->rows) ++t;
+    auto tiles = [&](const GroupTile& g) {
+        return groups * (double)(int64_t)((rows + g.m - 1) / g.m) * (double)((a.N + g.n - 1) / g.n);
+    };
+    while (t != kGroupTiles && 2 * tiles(*t) <= cus()) --t;
+    return t->launch(a, st);
+}
+
 }  // namespace
 
 hipError_t launch_gemm_b128(const void* qa, const float* sa, const void* qw, const float* sw, void* y, int64_t M, int64_t N,
                             int64_t K, hipStream_t st) {
-    return launch({reinterpret_cast<const uint8_t*>(qa), sa, reinterpret_cast<const uint8_t*>(qw), sw,
+    return launch({nullptr, reinterpret_cast<const uint8_t*>(qa), sa, reinterpret_cast<const uint8_t*>(qw), sw,
                    reinterpret_cast<uint16_t*>(y), nullptr, nullptr, M, M, N, K, 1}, st);
 }
 
 // codes [M, K], then scales [M, K / 128]
-size_t linear_b128_workspace_bytes(int64_t M, int64_t, int64_t K) { return (size_t)M * K + (size_t)M * (K / 128) * 4; }
+size_t linear_b128_workspace_bytes(int64_t M, int64_t, int64_t K) {
+    return one_launch(M, K) ? 0 : (size_t)M * K + (size_t)M * (K / 128) * 4;
+}
 
 hipError_t launch_linear_b128(const void* x, const void* qw, const float* sw, void* y, int64_t M, int64_t N, int64_t K,
                               void* workspace, hipStream_t st) {
+    if (one_launch(M, K))
+        return launch_quant_rows({reinterpret_cast<const uint16_t*>(x), nullptr, nullptr, reinterpret_cast<const uint8_t*>(qw),
+                                  sw, reinterpret_cast<uint16_t*>(y), nullptr, nullptr, M, M, N, K, 1}, st);
     uint8_t* q = reinterpret_cast<uint8_t*>(workspace);
     float* s = reinterpret_cast<float*>(q + M * K);
     const hipError_t err = launch_quant_b128_act(x, M, K, q, s, st);
@@ -84,8 +118,8 @@ hipError_t launch_linear_b128(const void* x, const void* qw, const float* sw, vo
 hipError_t launch_gemm_b128_grouped(const void* qa, const float* sa, int64_t arows, const void* qw, const float* sw,
                                     void* y, const int32_t* offsets, const int32_t* rows, int64_t G, int64_t M, int64_t N,
                                     int64_t K, hipStream_t st) {
-    return launch({reinterpret_cast<const uint8_t*>(qa), sa, reinterpret_cast<const uint8_t*>(qw), sw,
-                   reinterpret_cast<uint16_t*>(y), offsets, rows, arows, M, N, K, (int)G}, st);
+    return launch_grouped({nullptr, reinterpret_cast<const uint8_t*>(qa), sa, reinterpret_cast<const uint8_t*>(qw), sw,
+                           reinterpret_cast<uint16_t*>(y), offsets, rows, arows, M, N, K, (int)G}, st);
 }
 
 }  // namespace mx

@@ -19,7 +19,7 @@
 // first operand: a lane's four results are four consecutive n of one m, which share one activation scale.
 #pragma once
 
-#include "mx_device.hpp"
+#include "fp8_device.hpp"
 
 namespace mx {
 namespace b128 {
@@ -49,6 +49,7 @@ __device__ __forceinline__ void buffer2lds4(__amdgpu_buffer_rsrc_t r, void* lds_
 }
 
 struct Args {
+    const uint16_t* x;      // BF16 [M, K] instead of qa and sa, for the kernel that quantizes
     const uint8_t* qa;      // [rows of A, K]
     const float* sa;        // [rows of A, K / 128]
     const uint8_t* qw;      // [groups, N, K]
@@ -84,118 +85,84 @@ __device__ __forceinline__ void store4(uint16_t* y, int64_t N, int64_t n, v4f v,
     }
 }
 
-// ---------------------------------------------------------------------------- few rows
-// One workgroup per 16 FN columns (and group); its W waves take contiguous parts of K and meet in LDS, summed in
-// wave order.  Operands go from memory to registers through a ring of D stages of one block; rows in chunks
-// of at most 16 FM.
-template <int FM, int FN>
+// ---------------------------------------------------------------------------- a row or two, quantized on the way
+// The layer for M <= 16 rows of BF16, in one launch: one workgroup per 16 columns; its W waves take contiguous parts of K
+// and meet in LDS, summed in wave order.  Every wave quantizes its part of the rows into LDS, bit for bit as the
+// quantizer kernel, while its first weights are on the way; weights go from memory to registers through a ring of
+// D stages of one block.  Every workgroup quantizes all rows, so this pays for very few of them only (measured at N =
+// 7168, K = 8192, quantizer launch included: M = 1 / 2 12.3 / 12.9 us against 14.2 / 14.3, M = 4 15.0 against 14.4).
 struct Stage {
-    uint4 w[FN][2], x[FM][2];
-    float sw[FN], sx[FM];
+    uint4 w[2];
+    float sw;
 };
 
-template <int FM, int FN, int W, int D>
-__global__ __launch_bounds__(64 * W) void rows_kernel(Args a) {
-    __shared__ v4f red[W][FN][FM][64];
+// codes of one row and wave, padded by a chunk so that rows start in different banks
+__host__ __device__ constexpr int quant_row_bytes(int blocks) { return blocks * 128 + 16; }
+// bytes of dynamic LDS: codes and scales of M rows
+__host__ inline int64_t quant_lds_bytes(int64_t M, int64_t K, int W) {
+    const int64_t per = (K / 128 + W - 1) / W;
+    return W * M * (per * 128 + 16 + per * 4);
+}
+
+template <int W, int D>
+__global__ __launch_bounds__(64 * W) void quant_rows_kernel(Args a) {
+    __shared__ v4f red[W][64];
+    extern __shared__ __attribute__((aligned(16))) uint8_t codes[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, g = lane >> 4;
+    const int l16 = lane & 15, g = lane >> 4, M = (int)a.M;
     const int nkb = (int)(a.K / 128), per = (nkb + W - 1) / W;
     const int kb0 = min(wave * per, nkb), nk = min(per, nkb - kb0);
-    const int64_t n0 = (int64_t)blockIdx.x * 16 * FN;
-    const int e = blockIdx.y;
-    int64_t r0 = 0, r1 = a.M;
-    if (a.offsets) group_rows(a, e, r0, r1);
-    const uint8_t* wp[FN];
-    const float* swp[FN];
-#pragma unroll
-    for (int f = 0; f < FN; ++f) {
-        const int64_t n = min(n0 + 16 * f + l16, a.N - 1);
-        wp[f] = a.qw + (e * a.N + n) * a.K + 16 * g + (int64_t)kb0 * 128;
-        swp[f] = a.sw + (e * ((a.N + 127) / 128) + min(n0 + 16 * f, a.N - 1) / 128) * nkb + kb0;
-    }
-    // rows m0 .. of a chunk with F fragments
-    auto chunk = [&](int64_t m0, auto fc) __attribute__((always_inline)) {
-        constexpr int F = decltype(fc)::value;
-        const uint8_t* ap[F];
-        const float* sap[F];
-#pragma unroll
-        for (int j = 0; j < F; ++j) {
-            const int64_t r = max(a_row(a, min(m0 + 16 * j + l16, r1 - 1)), (int64_t)0);
-            ap[j] = a.qa + r * a.K + 16 * g + (int64_t)kb0 * 128;
-            sap[j] = a.sa + r * nkb + kb0;
-        }
-        v4f acc[FN][F] = {};
-        Stage<F, FN> st[D];
-        auto load = [&](Stage<F, FN>& s, int i) __attribute__((always_inline)) {
-#pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                s.w[f][0] = ldg16(wp[f] + i * 128);
-                s.w[f][1] = ldg16(wp[f] + i * 128 + 64);
-                s.sw[f] = swp[f][i];
-            }
-#pragma unroll
-            for (int j = 0; j < F; ++j) {
-                s.x[j][0] = ldg16(ap[j] + i * 128);
-                s.x[j][1] = ldg16(ap[j] + i * 128 + 64);
-                s.sx[j] = sap[j][i];
-            }
-        };
-        auto compute = [&](const Stage<F, FN>& s) __attribute__((always_inline)) {
-#pragma unroll
-            for (int f = 0; f < FN; ++f)
-#pragma unroll
-                for (int j = 0; j < F; ++j) {
-                    const v4f p = block_mfma(operand(s.w[f][0], s.w[f][1]), operand(s.x[j][0], s.x[j][1]));
-                    const float sc = s.sx[j] * s.sw[f];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[f][j][i] = __builtin_fmaf(p[i], sc, acc[f][j][i]);
-                }
-        };
-        if (nk > 0) {
-            static_for<D - 1>([&](auto d) { load(st[decltype(d)::value], min((int)decltype(d)::value, nk - 1)); });
-            int i = 0;
-            for (; i + 2 * D - 2 < nk; i += D)  // every load of the round is of this wave's part
-                static_for<D>([&](auto dc) {
-                    constexpr int d = decltype(dc)::value;
-                    load(st[(d + D - 1) % D], i + d + D - 1);
-                    __builtin_amdgcn_sched_barrier(0);  // keep the load ahead of the products, D - 1 stages in flight
-                    compute(st[d]);
-                    __builtin_amdgcn_sched_barrier(0);
-                });
-            for (; i < nk; i += D)
-                static_for<D>([&](auto dc) {
-                    constexpr int d = decltype(dc)::value;
-                    if (i + d < nk) {
-                        if (i + d + D - 1 < nk) load(st[(d + D - 1) % D], i + d + D - 1);
-                        compute(st[d]);
-                    }
-                });
-        }
-#pragma unroll
-        for (int f = 0; f < FN; ++f)
-#pragma unroll
-            for (int j = 0; j < F; ++j) red[wave][f][j][lane] = acc[f][j];
-        __syncthreads();
-        for (int t = threadIdx.x; t < FN * F * 64; t += 64 * W) {
-            const int f = t / (F * 64), j = t / 64 % F, l = t % 64;
-            v4f s = red[0][f][j][l];
-#pragma unroll
-            for (int w = 1; w < W; ++w) s += red[w][f][j][l];
-            const int64_t m = m0 + 16 * j + (l & 15);
-            if (m < r1) {
-                const v4f zero = {0.f, 0.f, 0.f, 0.f};
-                store4(a.y + m * a.N, a.N, n0 + 16 * f + 4 * (l >> 4), a_row(a, m) >= 0 ? s : zero,
-                       a.N % 4 == 0 && ((uintptr_t)a.y & 7) == 0);
-            }
-        }
-        __syncthreads();
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const uint8_t* wp = a.qw + min(n0 + l16, a.N - 1) * a.K + 16 * g + (int64_t)kb0 * 128;
+    const float* swp = a.sw + n0 / 128 * nkb + kb0;
+    const int pitch = quant_row_bytes(per), r = min(l16, M - 1);
+    uint8_t* own = codes + wave * M * pitch;
+    float* scales = reinterpret_cast<float*>(codes + W * M * pitch) + wave * M * per;
+
+    v4f acc = {};
+    Stage st[D];
+    auto load = [&](Stage& s, int i) __attribute__((always_inline)) {
+        s.w[0] = ldg16(wp + i * 128);
+        s.w[1] = ldg16(wp + i * 128 + 64);
+        s.sw = swp[i];
     };
-    for (int64_t m0 = r0; m0 < r1; m0 += 16 * FM) {
-        const int left = (int)min((r1 - m0 + 15) / 16, (int64_t)FM);
-        static_for<FM>([&](auto fc) {
-            constexpr int F = decltype(fc)::value + 1;
-            if (left == F) chunk(m0, std::integral_constant<int, F>{});
-        });
+    auto compute = [&](const Stage& s, int i) __attribute__((always_inline)) {
+        const uint8_t* x = own + r * pitch + i * 128 + 16 * g;
+        const v4f p = block_mfma(operand(s.w[0], s.w[1]), operand(ldg16(x), ldg16(x + 64)));
+        const float sc = scales[r * per + i] * s.sw;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(p[k], sc, acc[k]);
+    };
+    if (nk > 0) {
+        static_for<D - 1>([&](auto d) { load(st[decltype(d)::value], min((int)decltype(d)::value, nk - 1)); });
+        __builtin_amdgcn_sched_barrier(0);
+        // 16 lanes per block of 128, four blocks of this wave's part at a time; only this wave reads them back
+        for (int b0 = 0; b0 < M * nk; b0 += 4) {
+            const int b = b0 + (lane >> 4);
+            if (b < M * nk) {
+                const int m = b / nk, i = b % nk;
+                const uint4 x = *reinterpret_cast<const uint4*>(a.x + m * a.K + (int64_t)(kb0 + i) * 128 + 8 * l16);
+                float s;
+                *reinterpret_cast<uint2*>(own + m * pitch + i * 128 + 8 * l16) = quant_block_bf16x8(x, s);
+                if (l16 == 0) scales[m * per + i] = s;
+            }
+        }
+        for (int i = 0; i < nk; i += D)
+            static_for<D>([&](auto dc) {
+                constexpr int d = decltype(dc)::value;
+                if (i + d < nk) {
+                    if (i + d + D - 1 < nk) load(st[(d + D - 1) % D], i + d + D - 1);
+                    compute(st[d], i + d);
+                }
+            });
+    }
+    red[wave][lane] = acc;
+    __syncthreads();
+    if (wave == 0) {
+        v4f s = red[0][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) s += red[w][lane];
+        if (l16 < M) store4(a.y + l16 * a.N, a.N, n0 + 4 * g, s, a.N % 4 == 0 && ((uintptr_t)a.y & 7) == 0);
     }
 }
 
@@ -205,9 +172,9 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(Args a) {
 // pass through a ring of S slots in LDS, filled by direct copies.
 //
 // Slot, per group: TM + TN rows of 128 bytes, chunk c of row r at place c ^ (r / 2 % 8), so that the 16 lanes of a
-// fragment's read touch 16 different bank groups.  Scales come in batches of eight blocks, three of them in
-// LDS: a copy takes 32 bytes from each of eight rows, and the copies of batch B travel with the codes of the
-// steps of batch B - 1, one per wave and step.  (Copying each step's scales, one 4-byte piece of a cache line per
+// fragment's read touch 16 different bank groups.  Scales come in batches of eight (or sixteen) blocks, three of
+// them in LDS: a copy takes 32 bytes from each of eight rows (64 from four), and the copies of batch B travel with
+// the codes of the steps of batch B - 1, one per wave and step.  (Copying each step's scales, one 4-byte piece of a cache line per
 // row, took as many line requests as the codes.)
 //
 // Step u of a wave, its first two weight fragments, its row fragments and its scales already in registers:
@@ -274,9 +241,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     constexpr int CA = (KG * TM / 8 + W - 1) / W, CW = (KG * TN / 8 + W - 1) / W;  // copies of eight rows per wave
     constexpr bool kAhead = S == 2 && TM * TN >= 256 * 128;                        // lines fetched ahead into L2
     constexpr int C = CA + CW + 1 + kAhead;                                        // and one of scales
-    constexpr int kPart = (TM + TN) * 128, kSlot = KG * kPart, kBatch = (TM + 8) * 32, kBatches = S * kSlot;
+    constexpr int kPart = (TM + TN) * 128, kSlot = KG * kPart, kBatches = S * kSlot;
+    // a batch of scales: BB blocks of TM rows and of up to eight weight blocks, in parts of 64 scales
+    constexpr int BB = KG == 4 ? 16 : 8, kBatch = (TM + 8) * BB * 4, kPer = 64 / BB, kParts = (TM + 8) / kPer;
     constexpr int kTable = kBatches + 3 * kBatch, kSink = kTable + (TM + 8) * 4, kLds = kSink + (kAhead ? 256 : 0);
-    constexpr int SB = 8 / KG;  // steps per batch of scales
+    constexpr int SB = BB / KG;  // steps per batch of scales
     // MFMAs of a step, and those ahead of its barrier; the copies issued behind the barrier that frees their slot (the
     // others follow in the next step, ahead of its barrier), and the MFMAs that those others are spread over
     constexpr int kMf = FN * FM, kFirst = (FN - 2) * FM;
@@ -284,7 +253,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     constexpr int kLate = C - kEarly, kSpan = 2 * kLate < kFirst ? 2 * kLate : kFirst;
     constexpr bool kOneBlock = 128 % (16 * FN) == 0;    // a wave's columns lie in one weight block
     constexpr int kFree = FM > 2 && FN < 8 ? 2 : FM > 1 ? 1 : 0;  // row fragments read into registers of their own
-    static_assert(TM / 8 + 1 <= SB * W && S <= SB, "a batch's copies in its steps, and its place free in time");
+    static_assert(kParts <= SB * W && S <= SB, "a batch's copies in its steps, and its place free in time");
     static_assert(kLds <= 160 * 1024 && (S - 1) * C < 64 && FN >= 2 && FN <= 8, "LDS, counters, weight scales");
     static_assert((KG - 1) * FM * FN * 1024 * WM * WN <= kBatches, "sums of the groups");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
@@ -327,10 +296,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
         src[i] = r * (uint32_t)a.K + 16 * ((lane & 7) ^ (row >> 1 & 7));
     }
     // the scale copy that this wave issues in step c of a batch
-    auto part_of = [&](int c) __attribute__((always_inline)) { return min((c & (SB - 1)) * W + wave, TM / 8); };
+    auto part_of = [&](int c) __attribute__((always_inline)) { return min((c & (SB - 1)) * W + wave, kParts - 1); };
     auto issue_scale = [&](int b, int q, uint32_t row) __attribute__((always_inline)) {  // part q of batch b; row: from the table
-        const uint32_t at = row + 4 * min(8 * b + (lane & 7), nkb - 1);
-        buffer2lds4(q < TM / 8 ? rsa : rsw, lds + kBatches + b % 3 * kBatch + q * 256, at, 0);
+        const uint32_t at = row + 4 * min(BB * b + (lane & (BB - 1)), nkb - 1);
+        buffer2lds4(q < TM / kPer ? rsa : rsw, lds + kBatches + b % 3 * kBatch + q * 256, at, 0);
     };
     // Lines fetched ahead into L2: the 32 tiles that an XCD runs at a time are four row tiles by eight column tiles, so each
     // fetches an eighth of its A rows and a quarter of its weight rows, one 4-byte piece of every line, two steps before
@@ -358,22 +327,22 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     const uint32_t c0 = 16 * (g ^ key), c1 = 16 * ((g + 4) ^ key);
     const uint32_t xrow = base + kg * kPart + (16 * FM * wm + l16) * 128, wrow = base + kg * kPart + TM * 128 + (16 * FN * wn + l16) * 128;
     const uint32_t x0 = xrow + c0, x1 = xrow + c1, w0 = wrow + c0, w1 = wrow + c1;
-    const uint32_t xs = base + kBatches + 32 * (16 * FM * wm + l16);
+    const uint32_t xs = base + kBatches + 4 * BB * (16 * FM * wm + l16);
     // weight scales: fragment f is in block (n / 128) of its first column; the wave's fragments touch two at most
     const int nw = (int)(t.n0 - nb0 * 128) + 16 * FN * wn;  // from the first block's start
-    const uint32_t ws = base + kBatches + 32 * (TM + nw / 128);
+    const uint32_t ws = base + kBatches + 4 * BB * (TM + nw / 128);
     const int cut = 8 - nw % 128 / 16;  // fragments f < cut are in the first of the two
-    const uint32_t trow = base + kTable + 4 * (lane >> 3);
+    const uint32_t trow = base + kTable + 4 * (lane / BB);
 
     v4f acc[FN][FM] = {};
     v4u wl[FN], wh[FN], xl[FM], xh[FM];
     uint32_t sx[FM], sw[2], row[1];
 
     __syncthreads();  // the table
-    for (int q = wave; q <= TM / 8; q += W) issue_scale(0, q, table[8 * q + (lane >> 3)]);
+    for (int q = wave; q < kParts; q += W) issue_scale(0, q, table[kPer * q + lane / BB]);
     uint32_t first[S];
 #pragma unroll
-    for (int s = 0; s < S; ++s) first[s] = table[8 * part_of(s) + (lane >> 3)];
+    for (int s = 0; s < S; ++s) first[s] = table[kPer * part_of(s) + lane / BB];
     wait_vmcnt<0>();
     static_for<S>([&](auto s) {
         static_for<C>([&](auto i) {
@@ -382,22 +351,22 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     });
     auto scales_at = [&](int u) __attribute__((always_inline)) {  // offset of step u's scales (this group's block) in the batches
         const int b = u * KG + kg;
-        return (uint32_t)((b >> 3) % 3 * kBatch + 4 * (b & 7));
+        return (uint32_t)(b / BB % 3 * kBatch + 4 * (b & (BB - 1)));
     };
     wait_vmcnt<(S - 2) * C + kEarly>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     static_for<2>([&](auto i) {
-        sw[i] = lds_read4(scales_at(0) + ws + 32 * i);
+        sw[i] = lds_read4(scales_at(0) + ws + 4 * BB * i);
         wl[i] = lds_read16_at<i * 2048>(w0);
         wh[i] = lds_read16_at<i * 2048>(w1);
     });
     static_for<FM>([&](auto j) {
-        sx[j] = lds_read4(scales_at(0) + xs + 512 * j);
+        sx[j] = lds_read4(scales_at(0) + xs + 64 * BB * j);
         xl[j] = lds_read16_at<j * 2048>(x0);
         xh[j] = lds_read16_at<j * 2048>(x1);
     });
-    row[0] = lds_read4(trow + 32 * part_of(S));
+    row[0] = lds_read4(trow + 4 * kPer * part_of(S));
     // ends a step: what is carried into the next one has arrived
     auto arrive = [&]() __attribute__((always_inline)) {
         lds_wait<0>();
@@ -458,9 +427,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (kFirst == 0) static_for<C>([&](auto q) { issue(u + S, s, q, row[0]); });
                 const uint32_t sat = scales_at(u + 1);
-                static_for<2>([&](auto q) { sw[q] = lds_read4(sat + ws + 32 * q); });
-                static_for<FM>([&](auto q) { sx[q] = lds_read4(sat + xs + 512 * q); });
-                nrow[0] = lds_read4(trow + 32 * part_of(u + 1 + S));
+                static_for<2>([&](auto q) { sw[q] = lds_read4(sat + ws + 4 * BB * q); });
+                static_for<FM>([&](auto q) { sx[q] = lds_read4(sat + xs + 64 * BB * q); });
+                nrow[0] = lds_read4(trow + 4 * kPer * part_of(u + 1 + S));
                 static_for<2>([&](auto q) {
                     nwl[q] = lds_read16_at<q * 2048>(w0 + next);
                     nwh[q] = lds_read16_at<q * 2048>(w1 + next);

@@ -18,16 +18,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// scale of a block from its largest magnitude bit pattern
-__device__ __forceinline__ float block_scale(uint32_t mag_max) {
-    if (mag_max >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-    const float s = __uint_as_float(mag_max) / 448.0f;
-    return s == 0.0f ? 1.0f : s;
-}
-__device__ __forceinline__ float clamped_quotient(float x, float s) {
-    return __builtin_amdgcn_fmed3f(x / s, -448.0f, 448.0f);
-}
-
 // BF16 activations: 16 lanes own one block, 8 values (one 16-byte load, one 8-byte store) each, so a
 // wave reads 1 KB and writes 512 bytes, both contiguous; the maximum over the 16 lanes is four DPP
 // swaps.  Blocks are consecutive in memory whatever the row length, so the grid runs over blocks.
@@ -35,35 +25,9 @@ __global__ __launch_bounds__(kThreads) void quant_b128_act_kernel(const uint4* _
                                                                   float* __restrict__ s, int64_t units) {
     const int64_t stride = (int64_t)gridDim.x * kThreads;
     for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += stride) {
-        const uint4 r = x[u];
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-        uint32_t mag = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mag = max(mag, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
-        mag = row16_max(mag);  // units and the stride are multiples of 16: the lanes of a block run together
-        const float sc = block_scale(mag);
+        float sc;
+        q[u] = quant_block_bf16x8(x[u], sc);  // units and the stride are multiples of 16: the lanes of a block run together
         if ((threadIdx.x & 15) == 0) s[u >> 4] = sc;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-        uint2 out;
-        if (mag >= 0x7f800000u) {
-            out = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-        } else {
-            if (sc >= 0x1p-90f) {
-                const float rc = 1.0f / sc;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = div_corrected(v[i], sc, rc);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = clamped_quotient(v[i], sc);
-            }
-            out = make_uint2(e4m3fn_x4(v[0], v[1], v[2], v[3]), e4m3fn_x4(v[4], v[5], v[6], v[7]));
-        }
-        q[u] = out;
     }
 }
 

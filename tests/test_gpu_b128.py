@@ -84,6 +84,7 @@ SHAPES = [
     (33, 100, 128), (48, 577, 1024), (64, 512, 8192), (65, 130, 512), (100, 33, 1280), (128, 256, 2048), (129, 129, 256),
     (200, 1000, 896), (256, 224, 1664), (300, 7, 384), (512, 520, 640), (513, 300, 1152), (777, 1100, 2176), (1025, 513, 256),
     (2049, 260, 128), (1, 7168, 16384), (24, 2100, 16512), (700, 2900, 640),
+    (60, 7100, 256), (250, 7100, 640), (500, 7168, 1152), (1000, 7167, 256), (2049, 7168, 1280),  # every tile size
 ]
 
 
@@ -133,10 +134,10 @@ def test_gemm_every_code_and_scale_range(mx, orc, m):
     assert b128.accepts(bf16_host(y), ye, ad, b128.ANY).all()
 
 
-@pytest.mark.parametrize("m", [1, 40, 129, 640])
-def test_layer_is_quantizer_and_gemm(mx, orc, m):
+@pytest.mark.parametrize("m,n,k", [(1, 384, 1024), (1, 1, 128), (2, 37, 384), (2, 300, 5120), (1, 50, 16384), (2, 100, 16384),
+                                   (1, 130, 65536), (3, 384, 1024), (40, 384, 1024), (129, 384, 1024), (640, 384, 1024)])
+def test_layer_is_quantizer_and_gemm(mx, orc, m, n, k):
     import torch
-    n, k = 384, 1024
     x = _act(m, m, k)
     qw, sw = b128.quant_weight(orc, synth.weight_normal(m, n, k, 0.02))
     xd, qwd, swd = bf16_dev(x), to_dev(qw), to_dev(sw)
@@ -196,6 +197,7 @@ def _check_groups(orc, y, sizes, qa, sa, qw, sw, rows):
     ([0, 1, 17, 0, 5], 300, 512), ([3], 129, 256), ([1] * 20, 64, 384), ([40, 0, 33, 64, 2], 200, 1152),
     ([200, 3, 0, 129], 130, 640), ([0, 0, 500], 257, 256), ([700, 1000, 0, 33], 300, 384), ([0, 0], 16, 128),
     ([1300, 2, 600], 260, 256),
+    ([10, 0, 20, 31], 6000, 640), ([40, 0, 33, 64, 2], 4100, 384), ([200, 3, 0, 129], 4100, 1152), ([700, 1000, 0, 33], 4100, 256),
 ])
 @pytest.mark.parametrize("gather", [False, True])
 def test_grouped_matches_float64(mx, orc, sizes, n, k, gather):
