@@ -101,8 +101,7 @@ def test_gemm_matches_float64(mx, orc, m, n, k):
     buf = torch.full((m * n + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
     y = mx.gemm_a8w8_b128(to_dev(qa), to_dev(sa), to_dev(qw), to_dev(sw), y=buf[:m * n].view(m, n))
     ye, ad = b128.gemm(orc, qa, sa, qw, sw)
-    ok = b128.accepts(bf16_host(y), ye, ad)
-    assert ok.all(), "%d of %d outside tolerance" % ((~ok).sum(), ok.size)
+    b128.check(bf16_host(y), ye, ad)
     assert torch.isnan(buf[m * n:].float()).all(), "wrote behind the output"
 
 
@@ -112,7 +111,7 @@ def test_gemm_unaligned_output(mx, orc, m, n, k):
     qa, sa, qw, sw = _gemm_case(orc, m, n, k)
     buf = torch.zeros(m * n + 1, dtype=torch.bfloat16, device="cuda")
     y = mx.gemm_a8w8_b128(to_dev(qa), to_dev(sa), to_dev(qw), to_dev(sw), y=buf[1:].view(m, n))
-    assert b128.accepts(bf16_host(y), *b128.gemm(orc, qa, sa, qw, sw)).all()
+    b128.check(bf16_host(y), *b128.gemm(orc, qa, sa, qw, sw))
 
 
 @pytest.mark.parametrize("m", [4, 50, 300, 700])
@@ -131,7 +130,7 @@ def test_gemm_every_code_and_scale_range(mx, orc, m):
     ye, ad = b128.gemm(orc, qa, sa, qw, sw)
     assert np.isnan(ye[:, 5]).all() and np.isnan(ye[m - 1]).all() and np.isnan(ye[:, 128:]).all() and np.isfinite(ye[0, 0])
     y = mx.gemm_a8w8_b128(to_dev(qa), to_dev(sa), to_dev(qw), to_dev(sw))
-    assert b128.accepts(bf16_host(y), ye, ad, b128.ANY).all()
+    assert b128.accepts(bf16_host(y), ye, ad).all()
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 384, 1024), (1, 1, 128), (2, 37, 384), (2, 300, 5120), (1, 50, 16384), (2, 100, 16384),
@@ -143,7 +142,7 @@ def test_layer_is_quantizer_and_gemm(mx, orc, m, n, k):
     xd, qwd, swd = bf16_dev(x), to_dev(qw), to_dev(sw)
     y = mx.linear_a8w8_b128(xd, qwd, swd)
     qa, sa = b128.quant_act(orc, x)
-    assert b128.accepts(bf16_host(y), *b128.gemm(orc, qa, sa, qw, sw)).all()
+    b128.check(bf16_host(y), *b128.gemm(orc, qa, sa, qw, sw))
     again = mx.linear_a8w8_b128(xd, qwd, swd)
     assert torch.equal(y.view(torch.int16), again.view(torch.int16))
 
