@@ -48,9 +48,9 @@ struct Tile {
 };
 const Tile kTiles[] = {
     {16, 32, 10.2, launch_tile<1, 2, 1, 1, 4, 4>},   {16, 64, 10.8, launch_tile<1, 4, 1, 1, 4, 3>},
-    {32, 64, 12.8, launch_tile<2, 4, 1, 1, 4, 3>},   {64, 64, 17.4, launch_tile<2, 4, 2, 1, 2, 4>},
-    {64, 128, 29.5, launch_tile<2, 4, 2, 2, 1, 4>},  {128, 128, 40.5, launch_tile<2, 4, 4, 2, 1, 3>},
-    {256, 128, 70.0, launch_tile<4, 4, 4, 2, 1, 2>}, {256, 256, 113.0, launch_tile<4, 8, 4, 2, 1, 2>},
+    {32, 64, 12.5, launch_tile<2, 4, 1, 1, 4, 3>},   {64, 64, 15.8, launch_tile<2, 4, 2, 1, 2, 4>},
+    {64, 128, 27.0, launch_tile<2, 4, 2, 2, 1, 4>},  {128, 128, 35.0, launch_tile<2, 4, 4, 2, 1, 3>},
+    {256, 128, 64.8, launch_tile<4, 4, 4, 2, 1, 2>}, {256, 256, 109.0, launch_tile<4, 8, 4, 2, 1, 2>},
 };
 // for groups of up to `rows` rows in the mean
 struct GroupTile {

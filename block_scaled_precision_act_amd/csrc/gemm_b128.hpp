@@ -175,14 +175,16 @@ __global__ __launch_bounds__(64 * W) void quant_rows_kernel(Args a) {
 // Slot, per group: TM + TN rows of 128 bytes, chunk c of row r at place c ^ (r / 2 % 8), so that the 16 lanes of a
 // fragment's read touch 16 different bank groups.  Scales come in batches of eight (or sixteen) blocks, three of
 // them in LDS: a copy takes 32 bytes from each of eight rows (64 from four), and the copies of batch B travel with
-// the codes of the steps of batch B - 1, one per wave and step.  (Copying each step's scales, one 4-byte piece of a cache line per
+// the codes of the steps of batch B - 1, one per wave and step.  The blocks of a row are permuted by the row's part of 16,
+// so that the 16 rows of a fragment lie in different banks.  (Copying each step's scales, one 4-byte piece of a cache line per
 // row, took as many line requests as the codes.)
 //
-// Step u of a wave, its first two weight fragments, its row fragments and its scales already in registers:
-//   1. weight fragments 0 .. FN - 3 times all row fragments, reading weight fragment f + 2 before fragment f is used;
+// Step u of a wave, its first weight fragment, its row fragments and its scales already in registers:
+//   1. all but the last two or three weight fragments times all row fragments, reading weight fragments ahead;
 //   2. every operand of the step is now in registers: wait for the copies of u + 1, one barrier;
-//   3. the last two weight fragments, row fragment by row fragment, reading the next step's scales, first two weight
-//      fragments and row fragments as registers fall free.
+//   3. the last weight fragments, row fragment by row fragment, reading the next step's scales, first weight fragment
+//      and row fragments as registers fall free.
+// With three fragments behind the barrier where registers allow, LDS reads spread evenly over the MFMAs.
 // So MFMAs run across the barrier.  The slot that the barrier frees is refilled with the copies of u + S, spread over the
 // MFMAs of 3 and of the next step's 1: issued in one burst they hold up the waves behind the address unit.  The FMAs that scale a product follow two
 // MFMAs behind it.
@@ -249,8 +251,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     constexpr int SB = BB / KG;  // steps per batch of scales
     // MFMAs of a step, and those ahead of its barrier; the copies issued behind the barrier that frees their slot (the
     // others follow in the next step, ahead of its barrier), and the MFMAs that those others are spread over
-    constexpr int kMf = FN * FM, kFirst = (FN - 2) * FM;
-    constexpr int kWish = kFirst == 0 ? C : kFirst >= 2 * C ? FM : 2 * FM, kEarly = kWish < C ? kWish : C;
+    constexpr int kLast = FN >= 6 ? 3 : 2, kAhd = FN - kLast, kPre = kAhd == 0 ? FN : 1;  // fragments behind, ahead of the barrier; read early
+    constexpr int kMf = FN * FM, kFirst = kAhd * FM, kRest = kMf - kFirst;
+    constexpr int kWish = kFirst == 0 ? C : kFirst >= 2 * C ? (kRest + 1) / 2 : kRest, kEarly = kWish < C ? kWish : C;
     constexpr int kLate = C - kEarly, kSpan = 2 * kLate < kFirst ? 2 * kLate : kFirst;
     constexpr bool kOneBlock = 128 % (16 * FN) == 0;    // a wave's columns lie in one weight block
     constexpr int kFree = FM > 2 && FN < 8 ? 2 : FM > 1 ? 1 : 0;  // row fragments read into registers of their own
@@ -298,10 +301,16 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     }
     // the scale copy that this wave issues in step c of a batch
     auto part_of = [&](int c) __attribute__((always_inline)) { return min((c & (SB - 1)) * W + wave, kParts - 1); };
-    auto issue_scale = [&](int b, int q, uint32_t row) __attribute__((always_inline)) {  // part q of batch b; row: from the table
-        const uint32_t at = row + 4 * min(BB * b + (lane & (BB - 1)), nkb - 1);
-        buffer2lds4(q < TM / kPer ? rsa : rsw, lds + kBatches + b % 3 * kBatch + q * 256, at, 0);
+    struct ScaleCopy {
+        uint32_t at;  // the lane's offset
+        int dst;
+        bool weights;
     };
+    auto scale_copy = [&](int b, int q, uint32_t row) __attribute__((always_inline)) {  // part q of batch b; row: from the table
+        return ScaleCopy{row + 4 * min(BB * b + ((lane & (BB - 1)) ^ (q & (16 / kPer - 1))), nkb - 1),
+                         kBatches + b % 3 * kBatch + q * 256, q >= TM / kPer};
+    };
+    auto issue_scale = [&](const ScaleCopy& c) __attribute__((always_inline)) { buffer2lds4(c.weights ? rsw : rsa, lds + c.dst, c.at, 0); };
     // Lines fetched ahead into L2: the 32 tiles that an XCD runs at a time are four row tiles by eight column tiles, so each
     // fetches an eighth of its A rows and a quarter of its weight rows, one 4-byte piece of every line, two steps before
     // the copies need them.  Without it every step waits for the first reader's miss.
@@ -314,8 +323,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     const __amdgpu_buffer_rsrc_t rahead = __builtin_amdgcn_make_buffer_rsrc((void*)ahead_base, (short)0, -1, kRawWord3);
     int ahead_at = min(kDistance * KG, nkb - 1) * 128;
     // copy i of the C that go with step u, into its slot (blocks past the end: the last one again)
-    auto issue = [&](int u, int slot, int i, uint32_t row) __attribute__((always_inline)) {
-        if (i == 0) issue_scale(u / SB + 1, part_of(u), row);
+    auto issue = [&](int u, int slot, int i, const ScaleCopy& sc) __attribute__((always_inline)) {
+        if (i == 0) issue_scale(sc);
         else if (i == CA + CW + 1) {
             buffer2lds4(rahead, lds + kSink, ahead, ahead_at);
             ahead_at = min(ahead_at + KG * 128, (nkb - 1) * 128);
@@ -340,30 +349,31 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     uint32_t sx[FM], sw[2], row[1];
 
     __syncthreads();  // the table
-    for (int q = wave; q < kParts; q += W) issue_scale(0, q, table[kPer * q + lane / BB]);
+    for (int q = wave; q < kParts; q += W) issue_scale(scale_copy(0, q, table[kPer * q + lane / BB]));
     uint32_t first[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) first[s] = table[kPer * part_of(s) + lane / BB];
     wait_vmcnt<0>();
     static_for<S>([&](auto s) {
         static_for<C>([&](auto i) {
-            if (s < S - 1 || i < kEarly) issue(s, s, i, first[s]);
+            if (s < S - 1 || i < kEarly) issue(s, s, i, scale_copy(1, part_of(s), first[s]));
         });
     });
-    auto scales_at = [&](int u) __attribute__((always_inline)) {  // offset of step u's scales (this group's block) in the batches
+    // offsets of step u's scales (this group's block) in the batches: the weights', and this lane's rows'
+    auto scales_at = [&](int u, int part) __attribute__((always_inline)) {
         const int b = u * KG + kg;
-        return (uint32_t)(b / BB % 3 * kBatch + 4 * (b & (BB - 1)));
+        return (uint32_t)(b / BB % 3 * kBatch + 4 * ((b & (BB - 1)) ^ part));
     };
     wait_vmcnt<(S - 2) * C + kEarly>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    static_for<2>([&](auto i) {
-        sw[i] = lds_read4(scales_at(0) + ws + 4 * BB * i);
+    static_for<2>([&](auto i) { sw[i] = lds_read4(scales_at(0, 0) + ws + 4 * BB * i); });
+    static_for<kPre>([&](auto i) {
         wl[i] = lds_read16_at<i * 2048>(w0);
         wh[i] = lds_read16_at<i * 2048>(w1);
     });
     static_for<FM>([&](auto j) {
-        sx[j] = lds_read4(scales_at(0) + xs + 64 * BB * j);
+        sx[j] = lds_read4(scales_at(0, l16 / kPer) + xs + 64 * BB * j);
         xl[j] = lds_read16_at<j * 2048>(x0);
         xh[j] = lds_read16_at<j * 2048>(x1);
     });
@@ -371,7 +381,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     // ends a step: what is carried into the next one has arrived
     auto arrive = [&]() __attribute__((always_inline)) {
         lds_wait<0>();
-        asm volatile("" : "+v"(wl[0]), "+v"(wh[0]), "+v"(wl[1]), "+v"(wh[1]));
+#pragma unroll
+        for (int i = 0; i < kPre; ++i) asm volatile("" : "+v"(wl[i]), "+v"(wh[i]));
         lds_tie(sx);
         lds_tie(sw);
         lds_tie(xl);
@@ -394,8 +405,16 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
 #pragma unroll
             for (int j = 0; j < FM; ++j) fx[j] *= fw0;
         }
+        ScaleCopy copy = {};
+        uint32_t sat = 0, xat = 0, tat = 0;  // addresses of the next step's scales and table entry
+        auto place = [&](int part) __attribute__((always_inline)) {
+            if (part == 0) copy = scale_copy((u + S) / SB + 1, part_of(u + S), row[0]);
+            if (part == 1) sat = scales_at(u + 1, 0) + ws, xat = scales_at(u + 1, l16 / kPer) + xs;
+            if (part == 2) tat = trow + 4 * kPer * part_of(u + 1 + S);
+        };
+        if constexpr (kFirst == 0) place(0), place(1), place(2);
         v4f p[3];
-        v4u nwl[2], nwh[2], nxl[kFree + 1], nxh[kFree + 1];
+        v4u nwl[kPre], nwh[kPre], nxl[kFree + 1], nxh[kFree + 1];
         uint32_t nrow[1];
         auto scale = [&](auto ic, int f, int j) __attribute__((always_inline)) {
             const v4f v = p[decltype(ic)::value % 3];
@@ -403,59 +422,76 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[f][j][i] = __builtin_fmaf(v[i], m, acc[f][j][i]);
         };
-        // MFMA i's fragments: weight-major, then the last two weight fragments row by row
-        auto fof = [](int i) constexpr { return i < kFirst ? i / FM : FN - 2 + (i - kFirst) % 2; };
-        auto jof = [](int i) constexpr { return i < kFirst ? i % FM : (i - kFirst) / 2; };
+        // MFMA i's fragments: weight-major, then the last weight fragments row by row
+        auto fof = [](int i) constexpr { return i < kFirst ? i / FM : kAhd + (i - kFirst) % kLast; };
+        auto jof = [](int i) constexpr { return i < kFirst ? i % FM : (i - kFirst) / kLast; };
+        // the last weight fragment whose reads are issued by the start of fragment f: two ahead, or evenly
+        auto upto = [](int f) constexpr {
+            const int even = kAhd == 0 ? 0 : ((f + 1) * (FN - 1) + kAhd - 1) / (kAhd == 0 ? 1 : kAhd), two = f + 2;
+            return f < 0 ? kPre - 1 : (even > two ? even : two) < FN - 1 ? (even > two ? even : two) : FN - 1;
+        };
         static_for<kMf>([&](auto ic) {
             constexpr int i = decltype(ic)::value, f = fof(i), j = jof(i);
-            if constexpr (i < kFirst && j == 0) {  // fragment f's reads were issued two fragments ago
-                if constexpr (f >= 2) {
-                    lds_wait<2>();
+            if constexpr (i < kFirst && j == 0) {
+                if constexpr (f >= kPre) {
+                    lds_wait<2 * (upto(f - 1) - f)>();
                     asm volatile("" : "+v"(wl[f]), "+v"(wh[f]));
                 }
-                wl[f + 2] = lds_read16_at<(f + 2) * 2048>(w0 + at);
-                wh[f + 2] = lds_read16_at<(f + 2) * 2048>(w1 + at);
+                static_for<upto(f) - upto(f - 1)>([&](auto q) {
+                    constexpr int r = upto(f - 1) + 1 + q;
+                    wl[r] = lds_read16_at<r * 2048>(w0 + at);
+                    wh[r] = lds_read16_at<r * 2048>(w1 + at);
+                });
                 __builtin_amdgcn_sched_barrier(0);
             }
             if constexpr (i == kFirst) {
-                if constexpr (FN > 2) {
+                if constexpr (kAhd > 0) {
                     lds_wait<0>();
-                    if constexpr (FN > 3) asm volatile("" : "+v"(wl[FN - 2]), "+v"(wh[FN - 2]));
-                    asm volatile("" : "+v"(wl[FN - 1]), "+v"(wh[FN - 1]));
+#pragma unroll
+                    for (int q = kAhd; q < FN; ++q) asm volatile("" : "+v"(wl[q]), "+v"(wh[q]));
                 }
                 wait_vmcnt<(S - 2) * C + kAhead>();  // the line fetch is the last of a step's copies
                 __builtin_amdgcn_s_barrier();
                 __builtin_amdgcn_sched_barrier(0);
-                if constexpr (kFirst == 0) static_for<C>([&](auto q) { issue(u + S, s, q, row[0]); });
-                const uint32_t sat = scales_at(u + 1);
-                static_for<2>([&](auto q) { sw[q] = lds_read4(sat + ws + 4 * BB * q); });
-                static_for<FM>([&](auto q) { sx[q] = lds_read4(sat + xs + 64 * BB * q); });
-                nrow[0] = lds_read4(trow + 4 * kPer * part_of(u + 1 + S));
-                static_for<2>([&](auto q) {
-                    nwl[q] = lds_read16_at<q * 2048>(w0 + next);
-                    nwh[q] = lds_read16_at<q * 2048>(w1 + next);
-                });
-                static_for<kFree>([&](auto q) {
-                    nxl[q] = lds_read16_at<(FM - kFree + q) * 2048>(x0 + next);
-                    nxh[q] = lds_read16_at<(FM - kFree + q) * 2048>(x1 + next);
-                });
-                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (kFirst == 0) static_for<C>([&](auto q) { issue(u + S, s, q, copy); });
             }
             p[i % 3] = block_mfma(operand(wl[f], wh[f]), operand(xl[j], xh[j]));
             __builtin_amdgcn_sched_barrier(0);  // the product two back is scaled behind this MFMA, not ahead of it
             if constexpr (i >= 2) scale(std::integral_constant<int, i - 2>{}, fof(i - 2), jof(i - 2));
+            // ahead of the barrier: what the reads and copies behind it need
+            if constexpr (kFirst > 0) static_for<3>([&](auto q) { if (i == q * kFirst / 3) place(q); });
+            // behind it: the next step's first weight fragments, last row fragments, scales and table entry, spread evenly
+            if constexpr (i >= kFirst) {
+                constexpr int kReads = kPre + kFree + 2 + FM + 1, k = i - kFirst;
+                static_for<(k + 1) * kReads / kRest - k * kReads / kRest>([&](auto z) {
+                    constexpr int q = k * kReads / kRest + z, x = q - kPre, c = x - kFree, r = c - 2;
+                    if constexpr (q < kPre) {
+                        nwl[q] = lds_read16_at<q * 2048>(w0 + next);
+                        nwh[q] = lds_read16_at<q * 2048>(w1 + next);
+                    } else if constexpr (x < kFree) {
+                        nxl[x] = lds_read16_at<(FM - kFree + x) * 2048>(x0 + next);
+                        nxh[x] = lds_read16_at<(FM - kFree + x) * 2048>(x1 + next);
+                    } else if constexpr (c < 2) {
+                        sw[c] = lds_read4(sat + 4 * BB * c);
+                    } else if constexpr (r < FM) {
+                        sx[r] = lds_read4(xat + 64 * BB * r);
+                    } else {
+                        nrow[0] = lds_read4(tat);
+                    }
+                });
+            }
             // copies: the slot of the step before, then this step's
             if constexpr (i < kSpan)
                 static_for<(i + 1) * kLate / kSpan - i * kLate / kSpan>(
-                    [&](auto q) { issue(u - 1 + S, (s + S - 1) % S, kEarly + i * kLate / kSpan + q, 0); });
+                    [&](auto q) { issue(u - 1 + S, (s + S - 1) % S, kEarly + i * kLate / kSpan + q, copy); });
             if constexpr (i >= kFirst && kFirst > 0) {
                 constexpr int k = i - kFirst;
-                static_for<(k + 1) * kEarly / (2 * FM) - k * kEarly / (2 * FM)>(
-                    [&](auto q) { issue(u + S, s, k * kEarly / (2 * FM) + q, row[0]); });
+                static_for<(k + 1) * kEarly / kRest - k * kEarly / kRest>(
+                    [&](auto q) { issue(u + S, s, k * kEarly / kRest + q, copy); });
             }
             // row fragment j is free one MFMA after its last use
-            if constexpr (i > kFirst + 1 && (i - kFirst) % 2 == 0 && (i - kFirst) / 2 - 1 < FM - kFree) {
-                constexpr int q = (i - kFirst) / 2 - 1;
+            if constexpr (i > kFirst && (i - kFirst) % kLast == 0 && (i - kFirst) / kLast - 1 < FM - kFree) {
+                constexpr int q = (i - kFirst) / kLast - 1;
                 xl[q] = lds_read16_at<q * 2048>(x0 + next);
                 xh[q] = lds_read16_at<q * 2048>(x1 + next);
             }
@@ -469,9 +505,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
         scale(std::integral_constant<int, kMf - 1>{}, fof(kMf - 1), jof(kMf - 1));
         __builtin_amdgcn_sched_barrier(0);
         lds_wait<0>();
-        asm volatile("" : "+v"(nwl[0]), "+v"(nwh[0]), "+v"(nwl[1]), "+v"(nwh[1]));
         lds_tie(nrow);
-        wl[0] = nwl[0], wh[0] = nwh[0], wl[1] = nwl[1], wh[1] = nwh[1], row[0] = nrow[0];
+        row[0] = nrow[0];
+#pragma unroll
+        for (int q = 0; q < kPre; ++q) {
+            asm volatile("" : "+v"(nwl[q]), "+v"(nwh[q]));
+            wl[q] = nwl[q], wh[q] = nwh[q];
+        }
 #pragma unroll
         for (int q = 0; q < kFree; ++q) {
             asm volatile("" : "+v"(nxl[q]), "+v"(nxh[q]));
