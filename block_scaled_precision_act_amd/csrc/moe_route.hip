@@ -4,11 +4,12 @@
 // packed rows are the choices sorted by (expert, t, j), a stable counting sort: counts[e], offsets[e + 1] =
 // offsets[e] + counts[e], rows[p] = t of packed row p (-1 behind the last), slots[t, j] = p (-1 for no choice).
 // Every step is integer arithmetic whose result does not depend on the order of the atomic additions.
-//   Up to kOneMax choices one workgroup does it all in LDS, in one launch.  Above, one kernel counts the
-// experts of every chunk of choices and a second one, a workgroup per chunk, sums the counts of the chunks
-// before its own and places its chunk.  Every workgroup reads all counts (chunks * E integers, from L2), all its
-// threads sharing them out by expert and chunk: with a few threads walking the chunks one after another, 131072
-// choices over 256 experts took 51 us.
+//   A workgroup places a chunk of the choices and needs every expert's count, in all and in the chunks before its own.
+// Up to kAllMax choices each workgroup counts all ids itself, in LDS: one launch, no workspace.  Above, one kernel
+// counts every chunk and a second one sums the counts of the chunks (chunks * E integers, read by every workgroup)
+// before it places.  LDS atomics bound the first form (about 35 cycles for 64 random ids), a chain of memory and LDS
+// latencies the second: 512 choices over 32 experts 4.9 us, 8192 over 160 9.2 us, 24594 over 160 10.5 us (17 us in one
+// launch), 131072 over 256 10.4 us.
 //
 // Balance loss.  p = softmax(logits[t]) over the experts, f_e = counts_e / sum(counts), n the tokens whose
 // mask is not 0: loss = coef * E * sum_e f_e * mean_t p_te = sum_t sum_e w_e p_te with w_e = coef E f_e / n, so
@@ -22,10 +23,11 @@ namespace mx {
 namespace {
 
 constexpr int kMaxE = 1024;
-constexpr int kOneThreads = 1024, kOneMax = 8192;
-constexpr int kThreads = 512, kChunk = 2048;  // choices per workgroup of the two-kernel form
+constexpr int kThreads = 512, kChunk = 2048;  // choices per workgroup
+constexpr int kAllMax = 8192;
 
-__device__ __forceinline__ int id_at(const void* ids, bool wide, int64_t i, int E) {
+// Choices are numbered in 32 bits: T * top <= 2^24.
+__device__ __forceinline__ int id_at(const void* ids, bool wide, int i, int E) {
     if (wide) {
         const int64_t v = reinterpret_cast<const int64_t*>(ids)[i];
         return v >= 0 && v < E ? (int)v : -1;
@@ -67,87 +69,13 @@ __device__ __forceinline__ int block_scan(int v, int* tmp, int& total) {
     return before + s - v;
 }
 
-// Counts the ids of choices c0 .. c1 - 1 into hist[W][E] (LDS, per wave: wave w takes the w-th part of
-// whole rounds of 64), and afterwards places them: place(i, p) with p the running position of i's
-// expert and wave, starting from what hist holds then.
-template <int W>
-struct Chunk {
-    const void* ids;
-    bool wide;
-    int E, bits;
-    int64_t a, b;  // this wave's choices
-    __device__ __forceinline__ Chunk(const void* ids_, bool wide_, int E_, int64_t c0, int64_t c1) : ids(ids_), wide(wide_), E(E_) {
-        bits = 32 - __builtin_clz(E > 1 ? E - 1 : 1);
-        const int wave = threadIdx.x >> 6;
-        const int64_t per = ((c1 - c0 + W - 1) / W + 63) / 64 * 64;
-        a = min(c0 + wave * per, c1);
-        b = min(a + per, c1);
-    }
-    __device__ __forceinline__ void count(int* hist) const {
-        int* h = hist + (threadIdx.x >> 6) * E;
-        for (int64_t i = a + (threadIdx.x & 63); i < b; i += 64) {
-            const int id = id_at(ids, wide, i, E);
-            if (id >= 0) atomicAdd(h + id, 1);
-        }
-    }
-    template <typename F>
-    __device__ __forceinline__ void place(int* hist, F&& put) const {
-        int* h = hist + (threadIdx.x >> 6) * E;
-        const int lane = threadIdx.x & 63;
-        for (int64_t i0 = a; i0 < b; i0 += 64) {
-            const int64_t i = i0 + lane;
-            const int id = i < b ? id_at(ids, wide, i, E) : -1;
-            const uint64_t m = same_id(id, bits);
-            const int before = __popcll(m & ((1ull << lane) - 1));
-            int base = 0;
-            if (id >= 0 && before == 0) base = atomicAdd(h + id, __popcll(m));  // one lane per id; its wave's own counter
-            base = __shfl(base, m ? __ffsll((unsigned long long)m) - 1 : lane);
-            if (i < b) put(i, id >= 0 ? base + before : -1);
-        }
-    }
-};
-
-__global__ __launch_bounds__(kOneThreads) void moe_route_one(const void* ids, bool wide, int64_t n, int top, int E,
-                                                             int32_t* counts, int32_t* offsets, int32_t* rows, int32_t* slots) {
-    constexpr int W = kOneThreads / 64;
-    __shared__ int hist[W * kMaxE];
-    __shared__ int tmp[W];
-    for (int i = threadIdx.x; i < W * E; i += kOneThreads) hist[i] = 0;
-    __syncthreads();
-    const Chunk<W> c(ids, wide, E, 0, n);
-    c.count(hist);
-    __syncthreads();
-    int mine = 0;  // thread e: expert e
-    if ((int)threadIdx.x < E)
-        for (int w = 0; w < W; ++w) mine += hist[w * E + threadIdx.x];
-    int total;
-    const int start = block_scan<kOneThreads>(mine, tmp, total);
-    if ((int)threadIdx.x < E) {
-        counts[threadIdx.x] = mine;
-        offsets[threadIdx.x] = start;
-        int p = start;
-        for (int w = 0; w < W; ++w) {
-            const int h = hist[w * E + threadIdx.x];
-            hist[w * E + threadIdx.x] = p;
-            p += h;
-        }
-    }
-    if (threadIdx.x == 0) offsets[E] = total;
-    __syncthreads();
-    c.place(hist, [&](int64_t i, int p) {
-        slots[i] = p;
-        if (p >= 0) rows[p] = (int)(i / top);
-    });
-    for (int64_t p = total + threadIdx.x; p < n; p += kOneThreads) rows[p] = -1;
-}
-
 // hist[c, e]: the choices of expert e in chunk c
-__global__ __launch_bounds__(kThreads) void moe_route_count(const void* ids, bool wide, int64_t n, int E, int* __restrict__ hist) {
+__global__ __launch_bounds__(kThreads) void moe_route_count(const void* ids, bool wide, int n, int E, int* __restrict__ hist) {
     __shared__ int h[kMaxE];
     for (int e = threadIdx.x; e < E; e += kThreads) h[e] = 0;
     __syncthreads();
-    const int64_t c0 = (int64_t)blockIdx.x * kChunk, c1 = min(c0 + kChunk, n);
-    for (int64_t i = c0 + threadIdx.x; i < c1; i += kThreads) {
+    const int c0 = blockIdx.x * kChunk, c1 = min(c0 + kChunk, n);
+    for (int i = c0 + threadIdx.x; i < c1; i += kThreads) {
         const int id = id_at(ids, wide, i, E);
         if (id >= 0) atomicAdd(h + id, 1);
     }
@@ -155,63 +83,111 @@ __global__ __launch_bounds__(kThreads) void moe_route_count(const void* ids, boo
     for (int e = threadIdx.x; e < E; e += kThreads) hist[(int64_t)blockIdx.x * E + e] = h[e];
 }
 
-__global__ __launch_bounds__(kThreads) void moe_route_place(const void* ids, bool wide, int64_t n, int top, int E,
+// Places chunk blockIdx.x.  hist: the chunks' counts, or null: this workgroup counts all ids.  Wave w takes the w-th
+// part of the chunk in rounds of 64, its ids in registers from the start: what the kernel waits for is memory.
+__global__ __launch_bounds__(kThreads) void moe_route_place(const void* ids, bool wide, int n, int top, int E,
                                                             const int* __restrict__ hist, int32_t* counts, int32_t* offsets,
                                                             int32_t* rows, int32_t* slots) {
-    constexpr int W = kThreads / 64, PER = kMaxE / kThreads;
+    constexpr int W = kThreads / 64, PER = kMaxE / kThreads, R = kChunk / kThreads;
     __shared__ int h[W * kMaxE], all[kMaxE], before[kMaxE];
     __shared__ int tmp[W];
-    const int chunk = blockIdx.x, chunks = gridDim.x;
+    const int chunk = blockIdx.x, chunks = gridDim.x, lane = threadIdx.x & 63;
+    const int bits = 32 - __builtin_clz(E > 1 ? E - 1 : 1);
+    const int c0 = chunk * kChunk, c1 = min(c0 + kChunk, n), i0 = c0 + (threadIdx.x >> 6) * (R * 64) + lane;
+    int id[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) id[k] = i0 + 64 * k < c1 ? id_at(ids, wide, i0 + 64 * k, E) : -1;
+    int* mine = h + (threadIdx.x >> 6) * E;  // the wave's counts, later the running places
     for (int i = threadIdx.x; i < W * E; i += kThreads) h[i] = 0;
     for (int e = threadIdx.x; e < E; e += kThreads) all[e] = before[e] = 0;
     __syncthreads();
-    const int64_t c0 = (int64_t)chunk * kChunk, c1 = min(c0 + kChunk, n);
-    const Chunk<W> c(ids, wide, E, c0, c1);
-    c.count(h);
-    // the counts of all chunks: thread t takes expert t % span of chunks t / span, t / span + parts, ...
-    const int bits = c.bits < 9 ? c.bits : 9, span = 1 << bits, parts = kThreads >> bits;  // kThreads = 512
-    for (int e = threadIdx.x & (span - 1); e < E; e += span) {
-        int sum = 0, low = 0;
-#pragma unroll 8
-        for (int b = threadIdx.x >> bits; b < chunks; b += parts) {
-            const int v = hist[(int64_t)b * E + e];
-            sum += v;
-            low += b < chunk ? v : 0;
+    if (hist) {
+        // thread t takes expert t % span of chunks t / span, t / span + parts, ...
+        const int sbits = bits < 9 ? bits : 9, span = 1 << sbits, parts = kThreads >> sbits;
+        static_assert(kThreads == 512, "span");
+        for (int e = threadIdx.x & (span - 1); e < E; e += span) {
+            int sum = 0, low = 0;
+#pragma unroll 16
+            for (int b = threadIdx.x >> sbits; b < chunks; b += parts) {
+                const int v = hist[(int64_t)b * E + e];
+                sum += v;
+                low += b < chunk ? v : 0;
+            }
+            atomicAdd(all + e, sum);
+            atomicAdd(before + e, low);
         }
-        atomicAdd(all + e, sum);
-        atomicAdd(before + e, low);
-    }
-    __syncthreads();
-    // thread t: experts PER t .. PER t + PER - 1
-    int sum = 0;
+    } else if (chunks > 1) {
+        constexpr int B = kAllMax / kThreads;
+        int other[B];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) sum += PER * (int)threadIdx.x + k < E ? all[PER * threadIdx.x + k] : 0;
+        for (int k = 0; k < B; ++k) {
+            const int i = threadIdx.x + k * kThreads;
+            other[k] = i < n ? id_at(ids, wide, i, E) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+            if (other[k] >= 0) {
+                atomicAdd(all + other[k], 1);
+                if ((int)threadIdx.x + k * kThreads < c0) atomicAdd(before + other[k], 1);
+            }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+        if (id[k] >= 0) atomicAdd(mine + id[k], 1);
+    __syncthreads();
+    // thread t: expert t, or experts 2 t and 2 t + 1
+    const int per = E > kThreads ? PER : 1;
+    static_assert(PER <= 2, "experts per thread");
+    int mine_all[PER] = {}, waves[PER][W] = {}, sum = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int e = per * threadIdx.x + k;
+        if (k >= per || e >= E) continue;
+#pragma unroll
+        for (int w = 0; w < W; ++w) waves[k][w] = h[w * E + e];
+        mine_all[k] = all[e];
+        if (chunks == 1) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) mine_all[k] += waves[k][w];
+        }
+        sum += mine_all[k];
+    }
     int total;
     int start = block_scan<kThreads>(sum, tmp, total);
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        const int e = PER * threadIdx.x + k;
-        if (e >= E) continue;
+        const int e = per * threadIdx.x + k;
+        if (k >= per || e >= E) continue;
         if (chunk == 0) {
-            counts[e] = all[e];
+            counts[e] = mine_all[k];
             offsets[e] = start;
         }
         int p = start + before[e];
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const int v = h[w * E + e];
             h[w * E + e] = p;
-            p += v;
+            p += waves[k][w];
         }
-        start += all[e];
+        start += mine_all[k];
     }
     if (chunk == 0 && threadIdx.x == 0) offsets[E] = total;
     __syncthreads();
-    c.place(h, [&](int64_t i, int p) {
-        slots[i] = p;
-        if (p >= 0) rows[p] = (int)(i / top);
-    });
-    for (int64_t p = max((int64_t)total, c0) + threadIdx.x; p < c1; p += kThreads) rows[p] = -1;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int i = i0 + 64 * k;
+        if (i - lane >= c1) break;  // the wave's
+        const uint64_t m = same_id(id[k], bits);
+        const int ahead = __popcll(m & ((1ull << lane) - 1));
+        int base = 0;
+        if (id[k] >= 0 && ahead == 0) base = atomicAdd(mine + id[k], __popcll(m));  // one lane per id; its wave's own counter
+        base = __shfl(base, m ? __ffsll((unsigned long long)m) - 1 : lane);
+        if (i < c1) {
+            const int p = id[k] >= 0 ? base + ahead : -1;
+            slots[i] = p;
+            if (p >= 0) rows[p] = (uint32_t)i / (uint32_t)top;
+        }
+    }
+    for (int p = max(total, c0) + threadIdx.x; p < c1; p += kThreads) rows[p] = -1;
 }
 
 // ---------------------------------------------------------------- balance loss
@@ -248,22 +224,26 @@ __device__ __forceinline__ float row_max(float v) {
     return row_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// Row t's softmax: lane j of L holds experts j, j + L, ...  A row with no logit above -infinity has no
-// probabilities (all 0); a NaN or +infinity makes the row NaN.
+// Row t's logits: lane j of L holds experts j, j + L, ...; -infinity past E, and everywhere if there is no such row.
 template <int L, int V, bool HALF>
-__device__ __forceinline__ void row_softmax(const void* logits, int64_t t, int E, float (&p)[V]) {
+__device__ __forceinline__ void row_load(const void* logits, bool live, int64_t t, int E, float (&p)[V]) {
     const int j = threadIdx.x & (L - 1);
-    float top = -__builtin_inff(), sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = j + i * L;
         p[i] = -__builtin_inff();
-        if (e < E) {
+        if (live && e < E) {
             if constexpr (HALF) p[i] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(logits)[t * E + e] << 16);
             else p[i] = reinterpret_cast<const float*>(logits)[t * E + e];
         }
-        top = fmaxf(top, p[i]);
     }
+}
+// Logits to probabilities.  A row with no logit above -infinity has none (all 0); a NaN or +infinity makes the row NaN.
+template <int L, int V>
+__device__ __forceinline__ void row_softmax(float (&p)[V]) {
+    float top = p[0], sum = 0.f;
+#pragma unroll
+    for (int i = 1; i < V; ++i) top = fmaxf(top, p[i]);
     top = row_max<L>(top);
     const float base = top == -__builtin_inff() ? 0.f : top;
 #pragma unroll
@@ -277,17 +257,20 @@ __device__ __forceinline__ void row_softmax(const void* logits, int64_t t, int E
     for (int i = 0; i < V; ++i) p[i] *= r;
 }
 
-// Workgroup sum in a fixed order
-template <typename T, int THREADS>
-__device__ __forceinline__ T block_sum(T v, T* tmp) {
+__device__ __forceinline__ uint32_t wave_sum(uint32_t v) {
+    return __float_as_uint(row_reduce<64>(__uint_as_float(v), [](float a, float b) {
+        return __uint_as_float(__float_as_uint(a) + __float_as_uint(b));  // lane swaps move bits, whatever they are
+    }));
+}
+// Sums over the workgroup, in a fixed order: of each wave by shuffles or lane swaps, then of the waves.
+__device__ __forceinline__ double block_sum(double v, double* tmp) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    __syncthreads();
     if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
     __syncthreads();
-    T s = tmp[0];
+    double s = tmp[0];
 #pragma unroll
-    for (int w = 1; w < THREADS / 64; ++w) s += tmp[w];
+    for (int w = 1; w < kLossThreads / 64; ++w) s += tmp[w];
     return s;
 }
 
@@ -297,29 +280,45 @@ __global__ __launch_bounds__(kLossThreads) void moe_balance_kernel(const void* _
                                                                    const int32_t* __restrict__ counts,
                                                                    const uint8_t* __restrict__ mask, float coef, float* loss,
                                                                    float* __restrict__ w, double* __restrict__ part) {
-    __shared__ int64_t tmp[kLossThreads / 64];
+    __shared__ uint32_t tmp[kLossThreads / 64][3];
     __shared__ double dtmp[kLossThreads / 64];
     const int j = threadIdx.x & (L - 1);
-    int64_t chosen = 0, live = 0;
-    for (int e = threadIdx.x; e < E; e += kLossThreads) chosen += counts[e];
-    chosen = block_sum<int64_t, kLossThreads>(chosen, tmp);
+    const int64_t per = kLossThreads / L, step = gridDim.x * per;  // rows per round of a workgroup, and of all
+    int64_t t = blockIdx.x * per + threadIdx.x / L;
+    auto is_live = [&](int64_t r) { return r < T && (!mask || mask[r] != 0); };
+    float next[V];
+    row_load<L, V, HALF>(logits, is_live(t), t, E, next);  // on its way while the counts are summed
+    // choices in all (their halves of 16 bits apart: 1024 counts of 31 bits need 41) and unmasked tokens
+    uint32_t low = 0, high = 0, unmasked = 0;
+    for (int e = threadIdx.x; e < E; e += kLossThreads) {
+        low += (uint32_t)counts[e] & 0xffffu;
+        high += (uint32_t)counts[e] >> 16;
+    }
     if (mask) {
         // 16 bytes at a time from the first aligned one; every workgroup counts them all
         const int64_t head = min((int64_t)(-(uintptr_t)mask & 15), T), vecs = (T - head) / 16;
         const uint4* v = reinterpret_cast<const uint4*>(mask + head);
+        auto bytes = [](uint32_t w) { return __popc((((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w) & 0x80808080u); };  // not 0
         for (int64_t i = threadIdx.x; i < vecs; i += kLossThreads) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int b = 0; b < 32; b += 8) live += (w[k] >> b & 0xff) != 0;
+            const uint4 m = v[i];
+            unmasked += bytes(m.x) + bytes(m.y) + bytes(m.z) + bytes(m.w);
         }
-        for (int64_t t = threadIdx.x; t < head; t += kLossThreads) live += mask[t] != 0;
-        for (int64_t t = head + 16 * vecs + threadIdx.x; t < T; t += kLossThreads) live += mask[t] != 0;
-        live = block_sum<int64_t, kLossThreads>(live, tmp);
-    } else {
-        live = T;
+        for (int64_t r = threadIdx.x; r < head; r += kLossThreads) unmasked += mask[r] != 0;
+        for (int64_t r = head + 16 * vecs + threadIdx.x; r < T; r += kLossThreads) unmasked += mask[r] != 0;
     }
+    low = wave_sum(low), high = wave_sum(high), unmasked = wave_sum(unmasked);
+    if ((threadIdx.x & 63) == 0) {
+        uint32_t* w = tmp[threadIdx.x >> 6];
+        w[0] = low, w[1] = high, w[2] = unmasked;
+    }
+    __syncthreads();
+    int64_t chosen = 0, live = 0;
+#pragma unroll
+    for (int w = 0; w < kLossThreads / 64; ++w) {
+        chosen += tmp[w][0] + ((int64_t)tmp[w][1] << 16);
+        live += tmp[w][2];
+    }
+    if (!mask) live = T;
     const double unit = chosen > 0 && live > 0 ? (double)coef * E / ((double)chosen * (double)live) : 0.0;
     float we[V];
 #pragma unroll
@@ -329,17 +328,17 @@ __global__ __launch_bounds__(kLossThreads) void moe_balance_kernel(const void* _
         if (blockIdx.x == 0 && (int)threadIdx.x < L && e < E) w[e] = we[i];
     }
     double sum = 0;
-    const int per = kLossThreads / L;  // rows per workgroup and round
-    for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < T; t0 += (int64_t)gridDim.x * per) {
-        const int64_t t = t0 + threadIdx.x / L;
-        if (t >= T || (mask && mask[t] == 0)) continue;
+    for (; t < T; t += step) {
         float p[V], s = 0.f;
-        row_softmax<L, V, HALF>(logits, t, E, p);
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = next[i];
+        row_load<L, V, HALF>(logits, is_live(t + step), t + step, E, next);  // while this row is reduced
+        row_softmax<L, V>(p);  // a masked row has no logits: no probabilities
 #pragma unroll
         for (int i = 0; i < V; ++i) s = __builtin_fmaf(p[i], we[i], s);
         sum += s;
     }
-    sum = block_sum<double, kLossThreads>(sum, dtmp);
+    sum = block_sum(sum, dtmp);
     if (threadIdx.x == 0) {
         if (gridDim.x == 1) *loss = (float)sum;
         else part[blockIdx.x] = sum;
@@ -349,7 +348,7 @@ __global__ __launch_bounds__(kLossThreads) void moe_balance_kernel(const void* _
 __global__ __launch_bounds__(kLossThreads) void moe_balance_finish(const double* __restrict__ part, int n, float* loss) {
     __shared__ double tmp[kLossThreads / 64];
     double s = (int)threadIdx.x < n ? part[threadIdx.x] : 0.0;
-    s = block_sum<double, kLossThreads>(s, tmp);
+    s = block_sum(s, tmp);
     if (threadIdx.x == 0) *loss = (float)s;
 }
 
@@ -363,18 +362,23 @@ __global__ __launch_bounds__(kLossThreads) void moe_balance_grad_kernel(const vo
     float we[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) we[i] = j + i * L < E ? w[j + i * L] : 0.f;
-    const int per = kLossThreads / L;
-    for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < T; t0 += (int64_t)gridDim.x * per) {
-        const int64_t t = t0 + threadIdx.x / L;
-        if (t >= T) continue;
+    const int64_t per = kLossThreads / L, step = gridDim.x * per;
+    int64_t t = blockIdx.x * per + threadIdx.x / L;
+    auto is_live = [&](int64_t r) { return r < T && (!mask || mask[r] != 0); };
+    float next[V];
+    bool next_live = is_live(t);
+    row_load<L, V, HALF>(logits, next_live, t, E, next);
+    for (; t < T; t += step) {
         float p[V], s = 0.f;
-        const bool live = !mask || mask[t] != 0;
-        if (live) {
-            row_softmax<L, V, HALF>(logits, t, E, p);
+        const bool live = next_live;
 #pragma unroll
-            for (int i = 0; i < V; ++i) s = __builtin_fmaf(p[i], we[i], s);
-            s = row_sum<L>(s);
-        }
+        for (int i = 0; i < V; ++i) p[i] = next[i];
+        next_live = is_live(t + step);
+        row_load<L, V, HALF>(logits, next_live, t + step, E, next);  // while this row is reduced
+        row_softmax<L, V>(p);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s = __builtin_fmaf(p[i], we[i], s);
+        s = row_sum<L>(s);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = j + i * L;
@@ -409,23 +413,20 @@ int64_t loss_blocks(int64_t T, int64_t E) {
 }  // namespace
 
 size_t moe_route_workspace_bytes(int64_t n, int64_t E) {
-    return n <= kOneMax ? 0 : (size_t)((n + kChunk - 1) / kChunk) * E * sizeof(int);
+    return n <= kAllMax ? 0 : (size_t)((n + kChunk - 1) / kChunk) * E * sizeof(int);
 }
 
 hipError_t launch_moe_route(const void* ids, bool wide, int64_t T, int64_t top, int64_t E, int32_t* counts, int32_t* offsets,
                             int32_t* rows, int32_t* slots, void* workspace, hipStream_t st) {
     const int64_t n = T * top;
-    if (n <= kOneMax) {
-        hipLaunchKernelGGL(moe_route_one, dim3(1), dim3(kOneThreads), 0, st, ids, wide, n, (int)top, (int)E, counts, offsets,
-                           rows, slots);
-        return hipGetLastError();
+    const dim3 grid((unsigned)(n > 0 ? (n + kChunk - 1) / kChunk : 1));
+    int* hist = n <= kAllMax ? nullptr : reinterpret_cast<int*>(workspace);
+    if (hist) {
+        hipLaunchKernelGGL(moe_route_count, grid, dim3(kThreads), 0, st, ids, wide, (int)n, (int)E, hist);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
     }
-    const dim3 grid((unsigned)((n + kChunk - 1) / kChunk));
-    int* hist = reinterpret_cast<int*>(workspace);
-    hipLaunchKernelGGL(moe_route_count, grid, dim3(kThreads), 0, st, ids, wide, n, (int)E, hist);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(moe_route_place, grid, dim3(kThreads), 0, st, ids, wide, n, (int)top, (int)E, hist, counts, offsets, rows,
+    hipLaunchKernelGGL(moe_route_place, grid, dim3(kThreads), 0, st, ids, wide, (int)n, (int)top, (int)E, hist, counts, offsets, rows,
                        slots);
     return hipGetLastError();
 }

@@ -189,6 +189,8 @@ def _stream():
 
 def _need(t, dtype, ndim, name):
     torch = _torch()
+    if type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype != dtype:
@@ -374,12 +376,12 @@ def linear_a8w8(x, qw, sw):
 # ------------------------------------------------------------------ block-128 FP8
 def _raw_stream(device):
     """The current stream's handle on `device`, which must be the current device: the library launches there."""
-    cuda = _torch().cuda
-    index = cuda.current_device()
+    # device and handle straight from torch's C layer: building its Stream object costs as much as a kernel launch
+    c = _torch()._C
+    index = c._cuda_getDevice()
     if device.index != index:
         raise ValueError("operands are on %s, the current device is cuda:%d" % (device, index))
-    # the handle itself: building torch's Stream object around it costs as much as a kernel launch
-    return _torch()._C._cuda_getCurrentRawStream(index)
+    return c._cuda_getCurrentRawStream(index)
 
 
 def _same_device(like, **others):
@@ -506,12 +508,12 @@ def moe_route(ids, experts):
     T, top = ids.shape
     if experts < 1:
         raise ValueError("experts must be positive")
-    n = T * top  # one allocation: four would cost more than the kernel
-    counts, offsets, rows, slots = torch.empty(2 * experts + 1 + 2 * n, dtype=torch.int32, device=ids.device).split_with_sizes(
-        (experts, experts + 1, n, n))
+    # one allocation for the scratch and the outputs: five would cost more than the kernel
+    n, need = T * top, lib().moe_route_workspace_bytes(T, top, experts)
+    scratch = (need + 15) // 16 * 4
+    ws, counts, offsets, rows, slots = torch.empty(scratch + 2 * experts + 1 + 2 * n, dtype=torch.int32,
+                                                   device=ids.device).split_with_sizes((scratch, experts, experts + 1, n, n))
     slots = slots.view(T, top)
-    need = lib().moe_route_workspace_bytes(T, top, experts)
-    ws = _scratch(need, ids.device)
     _ok(lib().moe_route(ids.data_ptr(), ids.element_size(), T, top, experts, counts.data_ptr(), offsets.data_ptr(),
                         rows.data_ptr(), slots.data_ptr(), ws.data_ptr() if need else None, need,
                         _raw_stream(ids.device)), "moe_route")
@@ -544,9 +546,9 @@ def moe_balance_loss(logits, counts, coef, mask=None):
     if counts.shape[0] != E:
         raise ValueError("counts must have one entry per expert")
     _same_device(logits, counts=counts)
-    loss, weights = torch.empty(1 + E, dtype=torch.float32, device=logits.device).split_with_sizes((1, E))
     need = lib().moe_balance_loss_workspace_bytes(T, E)
-    ws = _scratch(need, logits.device)
+    scratch = (need + 15) // 16 * 4
+    ws, loss, weights = torch.empty(scratch + 1 + E, dtype=torch.float32, device=logits.device).split_with_sizes((scratch, 1, E))
     _ok(lib().moe_balance_loss(logits.data_ptr(), dtype, T, E, counts.data_ptr(),
                                mask.data_ptr() if mask is not None else None, coef, loss.data_ptr(), weights.data_ptr(),
                                ws.data_ptr() if need else None, need, _raw_stream(logits.device)), "moe_balance_loss")

@@ -27,7 +27,7 @@ def _route(ids, e):
 
 @pytest.mark.parametrize("t,top,e", [
     (1, 1, 1), (1, 8, 8), (64, 8, 32), (63, 3, 7), (1000, 2, 1000), (8192, 1, 1024), (1025, 8, 3), (8191, 1, 5), (4097, 2, 64),
-    (1000, 9, 160), (20000, 8, 256), (65537, 1, 2), (300, 100, 1024),
+    (1000, 9, 160), (20000, 8, 256), (65537, 1, 2), (300, 100, 1024), (65536, 1, 1024), (2048, 1, 40), (2049, 1, 40), (40000, 3, 1000),
 ])
 @pytest.mark.parametrize("wide", [False, True])
 def test_route_exact(mx, t, top, e, wide):
@@ -49,7 +49,7 @@ def test_route_without_choices(mx, t, top, e):
     assert not counts.any() and not offsets.any() and (rows == -1).all() and (slots == -1).all() and slots.shape == (t, top)
 
 
-@pytest.mark.parametrize("t", [700, 30000])
+@pytest.mark.parametrize("t", [700, 30000, 70000])
 def test_route_one_expert_takes_all(mx, t):
     ids = np.full((t, 1), 17, np.int32)
     counts, offsets, rows, slots = (g.cpu().numpy() for g in mx.moe_route(to_dev(ids), 40))
