@@ -4,14 +4,14 @@
 // of one round of that tile (kTiles; measured at K = 8192 and N = 7168, us, launch taken off), so a small product fills the
 // CUs with small tiles and a large one is read least by large tiles.
 //
-// Grouped products stream the experts' weights, so a tile should hold a whole group: by the mean group's rows, with
-// steps down while the tiles would leave half of the CUs idle.  Measured with 32 experts of [2048, 7168], us:
-//   rows        2     8    16    32    64   128   256   512
-//   16 x 64    91   105   115
-//   32 x 128   98    98    98   123   171
-//   64 x 128        104   103   109   142   195   315
-//   128 x 128                   121   134   173   260   419
-//   256 x 256                               221   237   347
+// Grouped products stream the experts' weights, so a tile should hold a whole group and be wide: by the mean group's
+// rows, with steps down while the tiles would leave half of the CUs idle.  Measured with 32 experts of [2048, 7168], us:
+//   mean rows    2     4     8    16    32    64   128   256   512
+//   16 x 64     87    91
+//   32 x 128    79    85    87    98
+//   64 x 128    78    84    87    89   102   118
+//   128 x 128   86    90    90    93    97   116   142          405
+//   256 x 256                                129   130   219   332
 #include "gemm_b128.hpp"
 #include "launch.hpp"
 
@@ -52,15 +52,15 @@ const Tile kTiles[] = {
     {64, 128, 27.0, launch_tile<2, 4, 2, 2, 1, 4>},  {128, 128, 35.0, launch_tile<2, 4, 4, 2, 1, 3>},
     {256, 128, 64.8, launch_tile<4, 4, 4, 2, 1, 2>}, {256, 256, 109.0, launch_tile<4, 8, 4, 2, 1, 2>},
 };
-// for groups of up to `rows` rows in the mean
+// for groups of up to `rows` rows in the mean; the first one only where wider tiles would be too few
 struct GroupTile {
     double rows;
     int m, n;
     hipError_t (*launch)(const Args&, hipStream_t);
 };
 const GroupTile kGroupTiles[] = {
-    {6, 16, 64, launch_tile<1, 4, 1, 1, 4, 3>},     {24, 32, 128, launch_tile<2, 4, 1, 2, 2, 3>},
-    {48, 64, 128, launch_tile<2, 4, 2, 2, 1, 4>},   {192, 128, 128, launch_tile<2, 4, 4, 2, 1, 3>},
+    {0, 16, 64, launch_tile<1, 4, 1, 1, 4, 3>},    {10, 32, 128, launch_tile<2, 4, 1, 2, 2, 3>},
+    {24, 64, 128, launch_tile<2, 4, 2, 2, 1, 4>},  {90, 128, 128, launch_tile<2, 4, 4, 2, 1, 3>},
     {1e30, 256, 256, launch_tile<4, 8, 4, 2, 1, 2>},
 };
 

@@ -201,39 +201,60 @@ struct TileAt {
     bool live;
 };
 
+// Row tiles of TM rows of groups g0 .. g0 + 63, one group per lane: the lane's own, and their running sum.
+template <int TM>
+__device__ __forceinline__ int group_tiles(const Args& a, int g0, int64_t& r0, int64_t& r1, int& own) {
+    const int lane = threadIdx.x & 63;
+    r0 = r1 = 0;
+    if (g0 + lane < a.G) group_rows(a, g0 + lane, r0, r1);
+    own = r1 > r0 ? (int)((r1 - r0 + TM - 1) / TM) : 0;
+    int sum = own;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(sum, d);
+        if (lane >= d) sum += o;
+    }
+    return sum;
+}
+
 // Workgroup b's tile.  Consecutive workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of tiles,
-// and walks it in bands of four row tiles, so tiles that run together share operand panels in its L2.
+// and walks it in bands of four row tiles, so tiles that run together share operand panels in its L2.  Grouped: the row
+// tiles of all groups one after another; the grid has room for more than there are, and only those that there are are
+// dealt out (dealing out the whole grid left an XCD idle).
 template <int TM, int TN>
 __device__ __forceinline__ TileAt tile_of(const Args& a, int b, int tiles_m, int tiles_n) {
+    int64_t r0, r1;
+    int own;
+    if (a.offsets) {
+        int rows = 0;
+        for (int g0 = 0; g0 < a.G; g0 += 64)
+            rows += __builtin_amdgcn_readlane(group_tiles<TM>(a, g0, r0, r1, own), 63);
+        tiles_m = min(tiles_m, rows);
+    }
     const int T = tiles_m * tiles_n, T8 = T & ~7;
     const int L = b < T8 ? (b & 7) * (T8 >> 3) + (b >> 3) : b;
+    TileAt t = {0, 0, a.M, 0, 0, 0, b < T};
+    if (!t.live) return t;
     const int band = L / (4 * tiles_n), high = min(tiles_m - 4 * band, 4), rem = L - band * 4 * tiles_n;
-    int tm = 4 * band + rem % high;
-    TileAt t = {0, (int64_t)tm * TM, a.M, (int64_t)(rem / high) * TN, tm, rem / high, true};
+    t.tm = 4 * band + rem % high;
+    t.tn = rem / high;
+    t.m0 = (int64_t)t.tm * TM;
+    t.n0 = (int64_t)t.tn * TN;
     if (a.offsets == nullptr) return t;
-    const int lane = threadIdx.x & 63;
     t.live = false;
-    for (int g0 = 0; g0 < a.G; g0 += 64) {  // 64 groups at a time: running sum of their row tiles
-        int64_t r0 = 0, r1 = 0;
-        if (g0 + lane < a.G) group_rows(a, g0 + lane, r0, r1);
-        const int n = r1 > r0 ? (int)((r1 - r0 + TM - 1) / TM) : 0;
-        int sum = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
-        }
-        const uint64_t past = __ballot(sum > tm);
+    int left = t.tm;
+    for (int g0 = 0; g0 < a.G; g0 += 64) {
+        const int sum = group_tiles<TM>(a, g0, r0, r1, own);
+        const uint64_t past = __ballot(sum > left);
         if (past) {
             const int i = __builtin_ctzll(past);
-            t.e = __builtin_amdgcn_readfirstlane(g0 + i);
-            const int first = __shfl((int)r0, i), end = __shfl((int)r1, i), before = __shfl(sum - n, i);
-            t.m0 = __builtin_amdgcn_readfirstlane(first) + (int64_t)__builtin_amdgcn_readfirstlane(tm - before) * TM;
-            t.r1 = __builtin_amdgcn_readfirstlane(end);
+            t.e = g0 + i;
+            t.m0 = __builtin_amdgcn_readlane((int)r0, i) + (int64_t)(left - __builtin_amdgcn_readlane(sum - own, i)) * TM;
+            t.r1 = __builtin_amdgcn_readlane((int)r1, i);
             t.live = true;
             break;
         }
-        tm -= __shfl(sum, 63);
+        left -= __builtin_amdgcn_readlane(sum, 63);
     }
     return t;
 }

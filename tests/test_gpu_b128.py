@@ -196,7 +196,7 @@ def _check_groups(orc, y, sizes, qa, sa, qw, sw, rows):
     ([0, 1, 17, 0, 5], 300, 512), ([3], 129, 256), ([1] * 20, 64, 384), ([40, 0, 33, 64, 2], 200, 1152),
     ([200, 3, 0, 129], 130, 640), ([0, 0, 500], 257, 256), ([700, 1000, 0, 33], 300, 384), ([0, 0], 16, 128),
     ([1300, 2, 600], 260, 256),
-    ([10, 0, 20, 31], 6000, 640), ([40, 0, 33, 64, 2], 4100, 384), ([200, 3, 0, 129], 4100, 1152), ([700, 1000, 0, 33], 4100, 256),
+    ([10, 0, 5, 3] * 2, 3000, 640), ([10, 0, 20, 31], 6000, 640), ([40, 0, 33, 64, 2], 4100, 384), ([200, 3, 0, 129], 4100, 1152), ([700, 1000, 0, 33], 4100, 256),
 ])
 @pytest.mark.parametrize("gather", [False, True])
 def test_grouped_matches_float64(mx, orc, sizes, n, k, gather):
