@@ -417,11 +417,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     auto step = [&](int u, auto sc) __attribute__((always_inline)) {
         constexpr int s = decltype(sc)::value;
         constexpr uint32_t at = s * kSlot, next = (s + 1) % S * kSlot;
+        // a group's block past the end repeats the last one, times 0
+        const bool inside = KG == 1 || u * KG + kg < nkb;
         float fx[FM];
 #pragma unroll
-        for (int j = 0; j < FM; ++j) fx[j] = KG == 1 || u * KG + kg < nkb ? __uint_as_float(sx[j]) : 0.f;
-        const float fw0 = __uint_as_float(__builtin_amdgcn_readfirstlane(sw[0])),
-                    fw1 = __uint_as_float(__builtin_amdgcn_readfirstlane(sw[1]));
+        for (int j = 0; j < FM; ++j) fx[j] = inside ? __uint_as_float(sx[j]) : 0.f;
+        const float fw0 = inside ? __uint_as_float(__builtin_amdgcn_readfirstlane(sw[0])) : 0.f,
+                    fw1 = inside ? __uint_as_float(__builtin_amdgcn_readfirstlane(sw[1])) : 0.f;
         if constexpr (kOneBlock) {
 #pragma unroll
             for (int j = 0; j < FM; ++j) fx[j] *= fw0;

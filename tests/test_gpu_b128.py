@@ -270,3 +270,41 @@ def test_other_stream_and_graph_replays(mx, orc):
         torch.cuda.synchronize()
         for a, b in zip(out, want[i]):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16)), "replay %d" % i
+
+
+def test_calls_on_two_streams_at_once(mx, orc):
+    """Layers and grouped products in flight on two streams, each with its own inputs, do not disturb each other."""
+    import torch
+    n, k, g = 700, 2176, 3
+    qw, sw = _experts(orc, g, n, k)
+    qw, sw = to_dev(qw), to_dev(sw)
+    work = [(bf16_dev(_act(200 + m, m, k)), to_dev(np.array([0, m // 3, m // 2, m], np.int32))) for m in (2, 50, 333, 900)]
+
+    def run(x, off):
+        qa, sa = mx.quant_act_b128(x)
+        return mx.linear_a8w8_b128(x, qw[0], sw[0]), mx.gemm_a8w8_b128_grouped(qa, sa, qw, sw, off)
+    want = [run(*w) for w in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for i in range(8):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(run(*work[(i * 3 + i // 4) % 4]))
+    torch.cuda.synchronize()
+    for i, pair in enumerate(got):
+        for a, b in zip(pair, want[(i * 3 + i // 4) % 4]):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16)), "call %d" % i
+
+
+@pytest.mark.parametrize("m", [2, 60, 300])
+def test_infinite_scales_stay_infinite(mx, m):
+    """An infinite scale gives infinities where its block's sum is not 0, also where K ends inside a step of the kernels."""
+    import torch
+    n, k = 130, 640
+    q = torch.full((m, k), 0x38, dtype=torch.uint8, device="cuda")   # 1.0
+    qw = torch.full((n, k), 0x38, dtype=torch.uint8, device="cuda")
+    sa, sw = torch.ones((m, k // 128), device="cuda"), torch.ones((2, k // 128), device="cuda")
+    sa[0, 4] = float("inf")
+    sw[1, 4] = float("inf")
+    y = mx.gemm_a8w8_b128(q, sa, qw, sw).float()
+    assert torch.isinf(y[0]).all() and torch.isinf(y[:, 128:]).all() and (y[1:, :128] == 640).all()
