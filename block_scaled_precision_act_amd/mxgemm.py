@@ -391,21 +391,18 @@ def _same_device(like, **others):
             raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
 
 
-def _scratch(nbytes, device):
-    """Memory for one call, from torch's allocator, which keeps it apart from calls on other streams and in
-    captured graphs."""
-    return _torch().empty(nbytes, dtype=_torch().uint8, device=device) if nbytes else None
-
-
 def quant_act_b128(x, q=None, s=None):
     """BF16 [M, K] -> (E4M3fn codes uint8 [M, K], FP32 scales [M, K/128]), one scale per 128 K-values of a row."""
     torch = _torch()
     _need(x, torch.bfloat16, 2, "x")
     M, K = x.shape
-    q = _out(q, torch.uint8, (M, K), x, "q")
-    s = _out(s, torch.float32, (M, K // 128), x, "s")
-    _ok(lib().b128_quant_act_fp8(x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(), _raw_stream(x.device)),
-        "b128_quant_act_fp8")
+    device = x.device
+    q = torch.empty((M, K), dtype=torch.uint8, device=device) if q is None else _out(q, torch.uint8, (M, K), x, "q")
+    s = (torch.empty((M, K // 128), dtype=torch.float32, device=device) if s is None
+         else _out(s, torch.float32, (M, K // 128), x, "s"))
+    status = lib().b128_quant_act_fp8(x.data_ptr(), M, K, q.data_ptr(), s.data_ptr(), _raw_stream(device))
+    if status:
+        raise MxError(status, "b128_quant_act_fp8")
     return q, s
 
 
@@ -433,10 +430,14 @@ def gemm_a8w8_b128(qa, sa, qw, sw, y=None):
     N = qw.shape[0]
     if qw.shape[1] != K or sa.shape != (M, K // 128) or sw.shape != ((N + 127) // 128, K // 128):
         raise ValueError("inconsistent block-128 A8W8 operand shapes")
-    _same_device(qa, sa=sa, qw=qw, sw=sw)
-    y = _out(y, torch.bfloat16, (M, N), qa, "y")
-    _ok(lib().gemm_a8w8_b128_bf16(qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(), y.data_ptr(), M, N, K,
-                                  _raw_stream(qa.device)), "gemm_a8w8_b128_bf16")
+    device = qa.device
+    if not sa.device == qw.device == sw.device == device:
+        _same_device(qa, sa=sa, qw=qw, sw=sw)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=device) if y is None else _out(y, torch.bfloat16, (M, N), qa, "y")
+    status = lib().gemm_a8w8_b128_bf16(qa.data_ptr(), sa.data_ptr(), qw.data_ptr(), sw.data_ptr(), y.data_ptr(), M, N, K,
+                                       _raw_stream(device))
+    if status:
+        raise MxError(status, "gemm_a8w8_b128_bf16")
     return y
 
 
@@ -451,12 +452,16 @@ def linear_a8w8_b128(x, qw, sw, y=None):
     N = qw.shape[0]
     if qw.shape[1] != K or sw.shape != ((N + 127) // 128, K // 128):
         raise ValueError("inconsistent block-128 A8W8 layer shapes")
-    _same_device(x, qw=qw, sw=sw)
-    y = _out(y, torch.bfloat16, (M, N), x, "y")
+    device = x.device
+    if not qw.device == sw.device == device:
+        _same_device(x, qw=qw, sw=sw)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=device) if y is None else _out(y, torch.bfloat16, (M, N), x, "y")
     need = lib().linear_a8w8_b128_workspace_bytes(M, N, K)
-    ws = _scratch(need, x.device)
-    _ok(lib().linear_a8w8_b128_bf16(x.data_ptr(), qw.data_ptr(), sw.data_ptr(), y.data_ptr(), M, N, K,
-                                    ws.data_ptr() if need else None, need, _raw_stream(x.device)), "linear_a8w8_b128_bf16")
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    status = lib().linear_a8w8_b128_bf16(x.data_ptr(), qw.data_ptr(), sw.data_ptr(), y.data_ptr(), M, N, K,
+                                         ws.data_ptr() if need else None, need, _raw_stream(device))
+    if status:
+        raise MxError(status, "linear_a8w8_b128_bf16")
     return y
 
 
@@ -480,11 +485,15 @@ def gemm_a8w8_b128_grouped(qa, sa, qw, sw, offsets, rows=None, y=None):
     if (qw.shape[2] != K or sa.shape != (R, K // 128) or sw.shape != (G, (N + 127) // 128, K // 128)
             or offsets.shape[0] != G + 1):
         raise ValueError("inconsistent grouped block-128 A8W8 operand shapes")
-    _same_device(qa, sa=sa, qw=qw, sw=sw, offsets=offsets, rows=rows)
-    y = _out(y, torch.bfloat16, (T, N), qa, "y")
-    _ok(lib().gemm_a8w8_b128_grouped_bf16(qa.data_ptr(), sa.data_ptr(), R, qw.data_ptr(), sw.data_ptr(), y.data_ptr(),
-                                          offsets.data_ptr(), rows.data_ptr() if rows is not None else None, G, T, N, K,
-                                          _raw_stream(qa.device)), "gemm_a8w8_b128_grouped_bf16")
+    device = qa.device
+    if not sa.device == qw.device == sw.device == offsets.device == device or (rows is not None and rows.device != device):
+        _same_device(qa, sa=sa, qw=qw, sw=sw, offsets=offsets, rows=rows)
+    y = torch.empty((T, N), dtype=torch.bfloat16, device=device) if y is None else _out(y, torch.bfloat16, (T, N), qa, "y")
+    status = lib().gemm_a8w8_b128_grouped_bf16(qa.data_ptr(), sa.data_ptr(), R, qw.data_ptr(), sw.data_ptr(), y.data_ptr(),
+                                               offsets.data_ptr(), rows.data_ptr() if rows is not None else None, G, T, N,
+                                               K, _raw_stream(device))
+    if status:
+        raise MxError(status, "gemm_a8w8_b128_grouped_bf16")
     return y
 
 
@@ -514,9 +523,11 @@ def moe_route(ids, experts):
     ws, counts, offsets, rows, slots = torch.empty(scratch + 2 * experts + 1 + 2 * n, dtype=torch.int32,
                                                    device=ids.device).split_with_sizes((scratch, experts, experts + 1, n, n))
     slots = slots.view(T, top)
-    _ok(lib().moe_route(ids.data_ptr(), ids.element_size(), T, top, experts, counts.data_ptr(), offsets.data_ptr(),
-                        rows.data_ptr(), slots.data_ptr(), ws.data_ptr() if need else None, need,
-                        _raw_stream(ids.device)), "moe_route")
+    status = lib().moe_route(ids.data_ptr(), ids.element_size(), T, top, experts, counts.data_ptr(), offsets.data_ptr(),
+                             rows.data_ptr(), slots.data_ptr(), ws.data_ptr() if need else None, need,
+                             _raw_stream(ids.device))
+    if status:
+        raise MxError(status, "moe_route")
     return counts, offsets, rows, slots
 
 
@@ -545,13 +556,16 @@ def moe_balance_loss(logits, counts, coef, mask=None):
     T, E = logits.shape
     if counts.shape[0] != E:
         raise ValueError("counts must have one entry per expert")
-    _same_device(logits, counts=counts)
+    if counts.device != logits.device:
+        _same_device(logits, counts=counts)
     need = lib().moe_balance_loss_workspace_bytes(T, E)
     scratch = (need + 15) // 16 * 4
     ws, loss, weights = torch.empty(scratch + 1 + E, dtype=torch.float32, device=logits.device).split_with_sizes((scratch, 1, E))
-    _ok(lib().moe_balance_loss(logits.data_ptr(), dtype, T, E, counts.data_ptr(),
-                               mask.data_ptr() if mask is not None else None, coef, loss.data_ptr(), weights.data_ptr(),
-                               ws.data_ptr() if need else None, need, _raw_stream(logits.device)), "moe_balance_loss")
+    status = lib().moe_balance_loss(logits.data_ptr(), dtype, T, E, counts.data_ptr(),
+                                    mask.data_ptr() if mask is not None else None, coef, loss.data_ptr(),
+                                    weights.data_ptr(), ws.data_ptr() if need else None, need, _raw_stream(logits.device))
+    if status:
+        raise MxError(status, "moe_balance_loss")
     return loss, weights
 
 
@@ -565,9 +579,13 @@ def moe_balance_loss_grad(logits, weights, grad_loss, mask=None, dlogits=None):
     T, E = logits.shape
     if weights.shape[0] != E or grad_loss.shape[0] != 1:
         raise ValueError("weights must have one entry per expert and grad_loss one entry")
-    _same_device(logits, weights=weights, grad_loss=grad_loss)
-    dlogits = _out(dlogits, logits.dtype, (T, E), logits, "dlogits")
-    _ok(lib().moe_balance_loss_grad(logits.data_ptr(), dtype, T, E, weights.data_ptr(),
-                                    mask.data_ptr() if mask is not None else None, grad_loss.data_ptr(),
-                                    dlogits.data_ptr(), _raw_stream(logits.device)), "moe_balance_loss_grad")
+    device = logits.device
+    if not weights.device == grad_loss.device == device:
+        _same_device(logits, weights=weights, grad_loss=grad_loss)
+    dlogits = torch.empty_like(logits) if dlogits is None else _out(dlogits, logits.dtype, (T, E), logits, "dlogits")
+    status = lib().moe_balance_loss_grad(logits.data_ptr(), dtype, T, E, weights.data_ptr(),
+                                         mask.data_ptr() if mask is not None else None, grad_loss.data_ptr(),
+                                         dlogits.data_ptr(), _raw_stream(device))
+    if status:
+        raise MxError(status, "moe_balance_loss_grad")
     return dlogits
