@@ -4,14 +4,17 @@
 // of one round of that tile (kTiles; measured at K = 8192 and N = 7168, us, launch taken off), so a small product fills the
 // CUs with small tiles and a large one is read least by large tiles.
 //
-// Grouped products stream the experts' weights, so a tile should hold a whole group and be wide: by the mean group's
-// rows, with steps down while the tiles would leave half of the CUs idle.  Measured with 32 experts of [2048, 7168], us:
-//   mean rows    2     4     8    16    32    64   128   256   512
-//   16 x 64     87    91
-//   32 x 128    79    85    87    98
-//   64 x 128    78    84    87    89   102   118
-//   128 x 128   86    90    90    93    97   116   142          405
-//   256 x 256                                129   130   219   332
+// Grouped products take theirs by the same rule from the mean group (kGroupTiles; rounds at K = 7168 with weights from HBM),
+// but not below the time that the weights take from memory at 5.4 TB/s; equal ones go to the larger tile.  Groups differ
+// in size, so a group is counted as rows / height + 0.4 row tiles, one at least.  Over 90 measured combinations of 8 to 64
+// groups, N 512 to 2048, K 2048 to 7168 and mean groups of 1 to 1024 rows (sizes off by 35%) the choice takes 1% more
+// than the best tile, 19% at worst.  Some of them, 32 experts of [2048, 7168] and 8 of [2048, 7168], us:
+//   mean rows        4    16    32    64   128   256   512  1024  |    4    16    64   256   512  1024
+//   16 x 64         92   109   177   306   449   724                26    36    81
+//   32 x 128        86    88   122   176   245   376   722          33    32    54    95
+//   64 x 128        86    89    92   141   184   287   513   950    35    32    36    85   142   202
+//   128 x 128       90    93    94   137   149   227   418   714    41    38    45    80   117   155
+//   256 x 256       92    92    96   110   126   220   331   555    72    72    88   103   108   110
 #include "gemm_b128.hpp"
 #include "launch.hpp"
 
@@ -40,6 +43,15 @@ hipError_t launch_tile(const Args& a, hipStream_t st) {
                        (int)tm, (int)tn);
     return hipGetLastError();
 }
+template <int FN, int WM, int WN, int S>
+hipError_t launch_heights(const Args& a, hipStream_t st) {
+    constexpr int TM = 64 * WM, TN = 16 * FN * WN;
+    const int64_t tm = a.M / TM + (a.G < a.M ? a.G : a.M), tn = (a.N + TN - 1) / TN;
+    if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((b128::tile_kernel_heights<FN, WM, WN, S>), dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), 0, st, a, (int)tm,
+                       (int)tn);
+    return hipGetLastError();
+}
 
 struct Tile {
     int m, n;
@@ -52,17 +64,12 @@ const Tile kTiles[] = {
     {64, 128, 27.0, launch_tile<2, 4, 2, 2, 1, 4>},  {128, 128, 35.0, launch_tile<2, 4, 4, 2, 1, 3>},
     {256, 128, 64.8, launch_tile<4, 4, 4, 2, 1, 2>}, {256, 256, 109.0, launch_tile<4, 8, 4, 2, 1, 2>},
 };
-// for groups of up to `rows` rows in the mean; the first one only where wider tiles would be too few
-struct GroupTile {
-    double rows;
-    int m, n;
-    hipError_t (*launch)(const Args&, hipStream_t);
+const Tile kGroupTiles[] = {
+    {16, 64, 12.0, launch_tile<1, 4, 1, 1, 4, 3>},   {32, 128, 24.0, launch_tile<2, 4, 1, 2, 2, 3>},
+    {64, 128, 34.0, launch_tile<2, 4, 2, 2, 1, 4>},  {128, 128, 46.0, launch_tile<2, 4, 4, 2, 1, 3>},
+    {256, 256, 100.0, launch_heights<8, 4, 2, 2>},
 };
-const GroupTile kGroupTiles[] = {
-    {0, 16, 64, launch_tile<1, 4, 1, 1, 4, 3>},    {10, 32, 128, launch_tile<2, 4, 1, 2, 2, 3>},
-    {24, 64, 128, launch_tile<2, 4, 2, 2, 1, 4>},  {90, 128, 128, launch_tile<2, 4, 4, 2, 1, 3>},
-    {1e30, 256, 256, launch_tile<4, 8, 4, 2, 1, 2>},
-};
+constexpr double kWeightBytesPerUs = 5.4e6;
 
 int cus() { return device_cus() > 0 ? device_cus() : 256; }
 
@@ -82,13 +89,19 @@ hipError_t launch(const Args& a, hipStream_t st) {
 
 hipError_t launch_grouped(const Args& a, hipStream_t st) {
     const double groups = (double)(a.G < a.M ? a.G : a.M), rows = (double)a.M / groups;
-    const GroupTile* t = kGroupTiles;
-    while (rows > t->rows) ++t;
-    auto tiles = [&](const GroupTile& g) {
-        return groups * (double)(int64_t)((rows + g.m - 1) / g.m) * (double)((a.N + g.n - 1) / g.n);
-    };
-    while (t != kGroupTiles && 2 * tiles(*t) <= cus()) --t;
-    return t->launch(a, st);
+    const double stream = groups * (double)a.N * (double)a.K / kWeightBytesPerUs;
+    const Tile* best = nullptr;
+    double least = 0;
+    for (const Tile& t : kGroupTiles) {
+        const double high = rows / t.m + 0.4;
+        const double tiles = groups * (high > 1 ? high : 1) * (double)((a.N + t.n - 1) / t.n);
+        const double work = __builtin_ceil(tiles / cus()) * t.round * ((double)a.K / 7168), time = work > stream ? work : stream;
+        if (!best || time <= least) {
+            best = &t;
+            least = time;
+        }
+    }
+    return best->launch(a, st);
 }
 
 }  // namespace

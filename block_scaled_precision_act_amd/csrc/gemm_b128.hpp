@@ -198,16 +198,20 @@ struct TileAt {
     int64_t m0, r1;   // first row, end of the group's rows
     int64_t n0;
     int tm, tn;       // row and column tile
+    int height;       // rows
     bool live;
 };
 
-// Row tiles of TM rows of groups g0 .. g0 + 63, one group per lane: the lane's own, and their running sum.
-template <int TM>
-__device__ __forceinline__ int group_tiles(const Args& a, int g0, int64_t& r0, int64_t& r1, int& own) {
+// Row tiles of groups g0 .. g0 + 63, one group per lane: the lane's own, their height, and the running sum of tiles.  A
+// group takes as few tiles of up to TM rows as it can, all of one height, the least multiple of STEP that does.
+template <int TM, int STEP>
+__device__ __forceinline__ int group_tiles(const Args& a, int g0, int64_t& r0, int64_t& r1, int& own, int& height) {
     const int lane = threadIdx.x & 63;
     r0 = r1 = 0;
     if (g0 + lane < a.G) group_rows(a, g0 + lane, r0, r1);
     own = r1 > r0 ? (int)((r1 - r0 + TM - 1) / TM) : 0;
+    height = TM;
+    if constexpr (STEP < TM) height = own > 0 ? (int)(((r1 - r0 + own - 1) / own + STEP - 1) / STEP * STEP) : TM;
     int sum = own;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -221,19 +225,19 @@ __device__ __forceinline__ int group_tiles(const Args& a, int g0, int64_t& r0, i
 // and walks it in bands of four row tiles, so tiles that run together share operand panels in its L2.  Grouped: the row
 // tiles of all groups one after another; the grid has room for more than there are, and only those that there are are
 // dealt out (dealing out the whole grid left an XCD idle).
-template <int TM, int TN>
+template <int TM, int TN, int STEP>
 __device__ __forceinline__ TileAt tile_of(const Args& a, int b, int tiles_m, int tiles_n) {
     int64_t r0, r1;
-    int own;
+    int own, height;
     if (a.offsets) {
         int rows = 0;
         for (int g0 = 0; g0 < a.G; g0 += 64)
-            rows += __builtin_amdgcn_readlane(group_tiles<TM>(a, g0, r0, r1, own), 63);
+            rows += __builtin_amdgcn_readlane(group_tiles<TM, STEP>(a, g0, r0, r1, own, height), 63);
         tiles_m = min(tiles_m, rows);
     }
     const int T = tiles_m * tiles_n, T8 = T & ~7;
     const int L = b < T8 ? (b & 7) * (T8 >> 3) + (b >> 3) : b;
-    TileAt t = {0, 0, a.M, 0, 0, 0, b < T};
+    TileAt t = {0, 0, a.M, 0, 0, 0, TM, b < T};
     if (!t.live) return t;
     const int band = L / (4 * tiles_n), high = min(tiles_m - 4 * band, 4), rem = L - band * 4 * tiles_n;
     t.tm = 4 * band + rem % high;
@@ -244,12 +248,13 @@ __device__ __forceinline__ TileAt tile_of(const Args& a, int b, int tiles_m, int
     t.live = false;
     int left = t.tm;
     for (int g0 = 0; g0 < a.G; g0 += 64) {
-        const int sum = group_tiles<TM>(a, g0, r0, r1, own);
+        const int sum = group_tiles<TM, STEP>(a, g0, r0, r1, own, height);
         const uint64_t past = __ballot(sum > left);
         if (past) {
             const int i = __builtin_ctzll(past);
             t.e = g0 + i;
-            t.m0 = __builtin_amdgcn_readlane((int)r0, i) + (int64_t)(left - __builtin_amdgcn_readlane(sum - own, i)) * TM;
+            t.height = __builtin_amdgcn_readlane(height, i);
+            t.m0 = __builtin_amdgcn_readlane((int)r0, i) + (int64_t)(left - __builtin_amdgcn_readlane(sum - own, i)) * t.height;
             t.r1 = __builtin_amdgcn_readlane((int)r1, i);
             t.live = true;
             break;
@@ -259,8 +264,13 @@ __device__ __forceinline__ TileAt tile_of(const Args& a, int b, int tiles_m, int
     return t;
 }
 
+// one tile's bytes of LDS: the ring, three batches of scales, their table, a place for lines fetched ahead
+constexpr int tile_lds(int FM, int FN, int WM, int WN, int KG, int S) {
+    return S * KG * 16 * (FM * WM + FN * WN) * 128 + 3 * (16 * FM * WM + 8) * (KG == 4 ? 16 : 8) * 4 + (16 * FM * WM + 8) * 4 + 256;
+}
+
 template <int FM, int FN, int WM, int WN, int KG, int S>
-__global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void tile_kernel(Args a, int tiles_m, int tiles_n) {
+__device__ __forceinline__ void tile(const Args& a, const TileAt& t, uint8_t* lds) {
     constexpr int TM = 16 * FM * WM, TN = 16 * FN * WN, W = WM * WN * KG;
     constexpr int CA = (KG * TM / 8 + W - 1) / W, CW = (KG * TN / 8 + W - 1) / W;  // copies of eight rows per wave
     constexpr bool kAhead = S == 2 && TM * TN >= 256 * 128;                        // lines fetched ahead into L2
@@ -268,7 +278,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     constexpr int kPart = (TM + TN) * 128, kSlot = KG * kPart, kBatches = S * kSlot;
     // a batch of scales: BB blocks of TM rows and of up to eight weight blocks, in parts of 64 scales
     constexpr int BB = KG == 4 ? 16 : 8, kBatch = (TM + 8) * BB * 4, kPer = 64 / BB, kParts = (TM + 8) / kPer;
-    constexpr int kTable = kBatches + 3 * kBatch, kSink = kTable + (TM + 8) * 4, kLds = kSink + (kAhead ? 256 : 0);
+    constexpr int kTable = kBatches + 3 * kBatch, kSink = kTable + (TM + 8) * 4, kLds = kSink + 256;
     constexpr int SB = BB / KG;  // steps per batch of scales
     // MFMAs of a step, and those ahead of its barrier; the copies issued behind the barrier that frees their slot (the
     // others follow in the next step, ahead of its barrier), and the MFMAs that those others are spread over
@@ -279,14 +289,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
     constexpr bool kOneBlock = 128 % (16 * FN) == 0;    // a wave's columns lie in one weight block
     constexpr int kFree = FM > 2 && FN < 8 ? 2 : FM > 1 ? 1 : 0;  // row fragments read into registers of their own
     static_assert(kParts <= SB * W && S <= SB, "a batch's copies in its steps, and its place free in time");
-    static_assert(kLds <= 160 * 1024 && (S - 1) * C < 64 && FN >= 2 && FN <= 8, "LDS, counters, weight scales");
+    static_assert(kLds == tile_lds(FM, FN, WM, WN, KG, S) && kLds <= 160 * 1024 && (S - 1) * C < 64 && FN >= 2 && FN <= 8, "LDS, counters, weight scales");
     static_assert((KG - 1) * FM * FN * 1024 * WM * WN <= kBatches, "sums of the groups");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, g = lane >> 4, kg = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
     const int nkb = __builtin_amdgcn_readfirstlane((int)(a.K / 128)), steps = (nkb + KG - 1) / KG;
-    const TileAt t = tile_of<TM, TN>(a, blockIdx.x, tiles_m, tiles_n);
-    if (!t.live) return;
     const int64_t nblocks = (a.N + 127) / 128, nb0 = t.n0 / 128;
 
     // Copies are buffer loads: a 32-bit offset per lane, the block of K in the scalar offset.  Rows are counted from the
@@ -575,6 +582,30 @@ __global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void 
             store4(a.y + m * a.N, a.N, t.n0 + 16 * (FN * wn + f) + 4 * g, ok ? acc[f][j] : zero, vec);
         }
     }
+}
+
+template <int FM, int FN, int WM, int WN, int KG, int S>
+__global__ __launch_bounds__(64 * WM * WN * KG, WM * WN * KG >= 8 ? 2 : 1) void tile_kernel(Args a, int tiles_m, int tiles_n) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[tile_lds(FM, FN, WM, WN, KG, S)];
+    constexpr int TM = 16 * FM * WM;
+    const TileAt t = tile_of<TM, 16 * FN * WN, TM>(a, blockIdx.x, tiles_m, tiles_n);
+    if (t.live) tile<FM, FN, WM, WN, KG, S>(a, t, lds);
+}
+
+// Groups of many rows: tiles of four heights, 16 WM to 64 WM.  A group's tiles being of one height keep step with each other,
+// so that its weights come from memory once.  Measured with 32 groups of N = 2048, K = 7168, against tiles of 256 rows only:
+// 384 rows each 198 instead of 243 us, 128 each 111 instead of 131, sizes about 512 (35% off) 328 instead of 337, 512
+// each no change.  (Tiles of 256 with the idle waves of a group's last one skipped lose step: 384 each 247.)
+template <int FN, int WM, int WN, int S>
+__global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel_heights(Args a, int tiles_m, int tiles_n) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[tile_lds(4, FN, WM, WN, 1, S)];
+    constexpr int STEP = 16 * WM;
+    const TileAt t = tile_of<4 * STEP, 16 * FN * WN, STEP>(a, blockIdx.x, tiles_m, tiles_n);
+    if (!t.live) return;
+    if (t.height == 4 * STEP) tile<4, FN, WM, WN, 1, S>(a, t, lds);
+    else if (t.height == 3 * STEP) tile<3, FN, WM, WN, 1, S>(a, t, lds);
+    else if (t.height == 2 * STEP) tile<2, FN, WM, WN, 1, S>(a, t, lds);
+    else tile<1, FN, WM, WN, 1, S>(a, t, lds);
 }
 
 }  // namespace b128

@@ -217,6 +217,23 @@ def test_grouped_matches_float64(mx, orc, sizes, n, k, gather):
     assert (y[total:].float() == 7.0).all()
 
 
+# tiles of all four heights (one, two and three of them to a group); more groups than a wave's lanes, few and many rows each
+@pytest.mark.parametrize("sizes,n,k", [
+    ([60, 120, 190, 250, 300, 0, 600, 30], 10000, 384), ([64, 65, 128, 129, 192, 193, 256, 257], 10000, 128),
+    ([(37 * i) % 260 for i in range(70)], 2048, 128), ([1] * 70 + [0] * 30 + [3] * 40, 64, 384), ([20, 5] * 40, 2000, 128),
+])
+def test_grouped_heights_and_many_groups(mx, orc, sizes, n, k):
+    import torch
+    total, arows = sum(sizes), 40
+    qw, sw = _experts(orc, len(sizes), n, k)
+    qa, sa = b128.quant_act(orc, _act(total + k, arows, k))
+    rows = np.random.default_rng(total).integers(0, arows, total).astype(np.int32)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    y = torch.full((total, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    mx.gemm_a8w8_b128_grouped(to_dev(qa), to_dev(sa), to_dev(qw), to_dev(sw), to_dev(off), rows=to_dev(rows), y=y)
+    _check_groups(orc, y, sizes, qa, sa, qw, sw, rows)
+
+
 @pytest.mark.parametrize("offsets", [[0, 5, 3, 40], [-3, 4, 9, 1000], [0, 0, 0, 0], [2, 6, 6, 20]])
 @pytest.mark.parametrize("t", [20, 400])
 def test_grouped_offsets_out_of_order_or_range(mx, orc, offsets, t):
