@@ -14,8 +14,9 @@
 // Balance loss.  p = softmax(logits[t]) over the experts, f_e = counts_e / sum(counts), n the tokens whose
 // mask is not 0: loss = coef * E * sum_e f_e * mean_t p_te = sum_t sum_e w_e p_te with w_e = coef E f_e / n, so
 // a row's share needs only its own logits, and the gradient is d loss / d logit_te = p_te (w_e - sum_j w_j p_tj).
-// 64, 32, 16 or 8 lanes hold a row in registers (one read of the logits each way; the kernels are bound by
-// that read, and by launches for few tokens).
+// 64, 32, 16 or 8 lanes hold a row in registers: one read of the logits each way.  Few tokens are bound by launches and the
+// chain of loads and reductions (T = 64, E = 32 in 3.7 us, gradient 2.3), many by memory: T = 16384, E = 256 FP32 masked, loss 10.5 us
+// (its second launch, which joins the workgroups' sums, 2.9 of it), gradient 8.9 (3.8 TB/s).
 #include "launch.hpp"
 #include "mx_device.hpp"
 
@@ -191,7 +192,8 @@ __global__ __launch_bounds__(kThreads) void moe_route_place(const void* ids, boo
 }
 
 // ---------------------------------------------------------------- balance loss
-constexpr int kLossThreads = 512, kLossBlocks = 512;
+constexpr int kLossThreads = 512, kLossBlocks = 1024;  // as many as fit at once
+constexpr int kRows = 2;                                // of a group of lanes at a time
 
 // Sums and maxima over the L lanes that hold a row (L = 8, 16, 32 or 64; every lane of them active), without LDS: lane
 // swaps within 16 lanes by DPP, then rows of 16 and halves of the wave exchanged.
@@ -224,19 +226,54 @@ __device__ __forceinline__ float row_max(float v) {
     return row_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// Row t's logits: lane j of L holds experts j, j + L, ...; -infinity past E, and everywhere if there is no such row.
-template <int L, int V, bool HALF>
-__device__ __forceinline__ void row_load(const void* logits, bool live, int64_t t, int E, float (&p)[V]) {
-    const int j = threadIdx.x & (L - 1);
+// A row as loaded: lane j of L holds experts j V .. j V + V - 1.  VEC: E is a multiple of V and rows start at multiples of their
+// loads (row_vec).  Every lane loads, those past E from a place inside the row, so that nothing branches between the loads of
+// two rows; values are taken out when they are needed.
+template <int L, int V, bool HALF, bool VEC>
+struct Row {
+    static constexpr int kBytes = V * (HALF ? 2 : 4), kLoad = kBytes < 16 ? kBytes : 16;  // of the lane; of a load
+    uint32_t w[VEC ? (kBytes + 3) / 4 : V];
+    __device__ __forceinline__ void load(const void* logits, int64_t t, int E) {
+        const int e0 = (threadIdx.x & (L - 1)) * V;
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(logits) + t * E;
+        const uint32_t* f = reinterpret_cast<const uint32_t*>(logits) + t * E;
+        if constexpr (VEC && kLoad > 2) {
+            const int at = min(e0, E - V);
+            const uint8_t* src = HALF ? reinterpret_cast<const uint8_t*>(h + at) : reinterpret_cast<const uint8_t*>(f + at);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = j + i * L;
-        p[i] = -__builtin_inff();
-        if (live && e < E) {
-            if constexpr (HALF) p[i] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(logits)[t * E + e] << 16);
-            else p[i] = reinterpret_cast<const float*>(logits)[t * E + e];
+            for (int c = 0; c < kBytes / kLoad; ++c)
+                __builtin_memcpy(w + c * kLoad / 4, __builtin_assume_aligned(src + c * kLoad, kLoad), kLoad);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[i] = HALF ? h[min(e0 + i, E - 1)] : f[min(e0 + i, E - 1)];
         }
     }
+    // -infinity past E, and everywhere in a row that is not live
+    __device__ __forceinline__ void take(bool live, int E, float (&p)[V]) const {
+        const int e0 = (threadIdx.x & (L - 1)) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            uint32_t v;
+            if constexpr (!HALF) v = w[i];
+            else if constexpr (VEC && V > 1) v = i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16;
+            else v = w[i] << 16;
+            p[i] = live && (VEC ? e0 : e0 + i) < E ? __uint_as_float(v) : -__builtin_inff();
+        }
+    }
+};
+template <int V, bool HALF>
+bool row_vec(const void* p, int64_t E) {
+    constexpr int B = V * (HALF ? 2 : 4);
+    return E % V == 0 && (uintptr_t)p % (B < 16 ? B : 16) == 0;
+}
+
+// e^d for d <= 0: the product with log2(e) in two parts, so off by little more than v_exp's last place; 0 below e^-87, where
+// a probability is far below the last place of any sum that it enters
+__device__ __forceinline__ float exp_neg(float d) {
+    constexpr float kLog2e = 1.44269504f, kLow = 1.92596299e-8f, kLn2 = 0.693147181f;
+    const float t = d * kLog2e, low = __builtin_fmaf(d, kLow, __builtin_fmaf(d, kLog2e, -t));
+    const float v = __builtin_amdgcn_exp2f(t);
+    return d < -87.f ? 0.f : __builtin_fmaf(v, low * kLn2, v);  // NaN stays NaN
 }
 // Logits to probabilities.  A row with no logit above -infinity has none (all 0); a NaN or +infinity makes the row NaN.
 template <int L, int V>
@@ -248,7 +285,7 @@ __device__ __forceinline__ void row_softmax(float (&p)[V]) {
     const float base = top == -__builtin_inff() ? 0.f : top;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        p[i] = expf(p[i] - base);
+        p[i] = exp_neg(p[i] - base);
         sum += p[i];
     }
     sum = row_sum<L>(sum);
@@ -262,132 +299,176 @@ __device__ __forceinline__ uint32_t wave_sum(uint32_t v) {
         return __uint_as_float(__float_as_uint(a) + __float_as_uint(b));  // lane swaps move bits, whatever they are
     }));
 }
-// Sums over the workgroup, in a fixed order: of each wave by shuffles or lane swaps, then of the waves.
-__device__ __forceinline__ double block_sum(double v, double* tmp) {
+
+// The loss and the experts' weights from the threads' shares of sum_t sum_e counts_e p_te and of the unmasked tokens.  All
+// sums in FP64 and in a fixed order: lanes, then waves.
+__device__ __forceinline__ void balance_finish(double sum, double live, const int32_t* __restrict__ counts, int E, float coef,
+                                               float* loss, float* __restrict__ w) {
+    __shared__ double tmp[3][kLossThreads / 64];
+    double v[3] = {sum, live, 0.0};
+    for (int e = threadIdx.x; e < E; e += kLossThreads) v[2] += counts[e];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
+    for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) v[i] += __shfl_xor(v[i], d);
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) tmp[i][threadIdx.x >> 6] = v[i];
+    }
     __syncthreads();
-    double s = tmp[0];
 #pragma unroll
-    for (int w = 1; w < kLossThreads / 64; ++w) s += tmp[w];
-    return s;
+    for (int i = 0; i < 3; ++i) {
+        v[i] = tmp[i][0];
+#pragma unroll
+        for (int k = 1; k < kLossThreads / 64; ++k) v[i] += tmp[i][k];
+    }
+    const double unit = v[2] > 0 && v[1] > 0 ? (double)coef * E / (v[2] * v[1]) : 0.0;
+    for (int e = threadIdx.x; e < E; e += kLossThreads) w[e] = (float)(unit * counts[e]);
+    if (threadIdx.x == 0) *loss = (float)(unit * v[0]);
 }
 
-// Every workgroup sums its rows' shares of the loss; part[b] (or the loss itself, when there is one workgroup).
+// Calls f(t, live, p) for the rows t of this lane's group of L, two at a time (their loads and reductions run beside each other);
+// p are the lane's probabilities.  A row that is not live, masked or past T - 1, has none.  T > 0.
+template <int L, int V, bool HALF, bool VEC, typename F>
+__device__ __forceinline__ void for_rows(const void* __restrict__ logits, int64_t T, int E, const uint8_t* __restrict__ mask, F&& f) {
+    const int64_t step = gridDim.x * (int64_t)(kLossThreads / L);  // rows per round
+    const uint8_t* bytes = mask ? mask : reinterpret_cast<const uint8_t*>(logits);  // without a mask, any bytes do
+    for (int64_t t = blockIdx.x * (int64_t)(kLossThreads / L) + threadIdx.x / L; t < T; t += kRows * step) {
+        Row<L, V, HALF, VEC> row[kRows];
+        uint8_t m[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int64_t u = min(t + k * step, T - 1);
+            row[k].load(logits, u, E);
+            m[k] = bytes[u];
+        }
+        float p[kRows][V];
+        bool live[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            live[k] = t + k * step < T && (!mask || m[k] != 0);
+            row[k].take(live[k], E, p[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) row_softmax<L, V>(p[k]);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) f(t + k * step, live[k], p[k]);
+    }
+}
+
+// Every workgroup sums its rows' shares and counts its unmasked rows, into part[2 b] and part[2 b + 1] for
+// moe_balance_finish; one workgroup alone finishes by itself.
 template <int L, int V, bool HALF>
-__global__ __launch_bounds__(kLossThreads) void moe_balance_kernel(const void* __restrict__ logits, int64_t T, int E,
+__global__ __launch_bounds__(kLossThreads) void moe_balance_kernel(const void* __restrict__ logits, int64_t T, int E, bool vec,
                                                                    const int32_t* __restrict__ counts,
                                                                    const uint8_t* __restrict__ mask, float coef, float* loss,
                                                                    float* __restrict__ w, double* __restrict__ part) {
-    __shared__ uint32_t tmp[kLossThreads / 64][3];
-    __shared__ double dtmp[kLossThreads / 64];
-    const int j = threadIdx.x & (L - 1);
-    const int64_t per = kLossThreads / L, step = gridDim.x * per;  // rows per round of a workgroup, and of all
-    int64_t t = blockIdx.x * per + threadIdx.x / L;
-    auto is_live = [&](int64_t r) { return r < T && (!mask || mask[r] != 0); };
-    float next[V];
-    row_load<L, V, HALF>(logits, is_live(t), t, E, next);  // on its way while the counts are summed
-    // choices in all (their halves of 16 bits apart: 1024 counts of 31 bits need 41) and unmasked tokens
-    uint32_t low = 0, high = 0, unmasked = 0;
-    for (int e = threadIdx.x; e < E; e += kLossThreads) {
-        low += (uint32_t)counts[e] & 0xffffu;
-        high += (uint32_t)counts[e] >> 16;
+    __shared__ double tmp[2][kLossThreads / 64];
+    const int e0 = (threadIdx.x & (L - 1)) * V;
+    int held[V];
+    float count[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) held[i] = counts[min(e0 + i, E - 1)];
+#pragma unroll
+    for (int i = 0; i < V; ++i) count[i] = e0 + i < E ? (float)held[i] : 0.f;
+    double sum = 0;
+    uint32_t live = 0;  // rows; the row's first lane counts
+    auto row = [&](int64_t, bool counted, const float (&p)[V]) __attribute__((always_inline)) {
+        float s = 0.f;
+        live += counted && e0 == 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s = __builtin_fmaf(p[i], count[i], s);
+        sum += s;
+    };
+    if (T > 0) {
+        if (V == 1 || !vec) for_rows<L, V, HALF, false>(logits, T, E, mask, row);
+        else for_rows<L, V, HALF, true>(logits, T, E, mask, row);
     }
-    if (mask) {
-        // 16 bytes at a time from the first aligned one; every workgroup counts them all
-        const int64_t head = min((int64_t)(-(uintptr_t)mask & 15), T), vecs = (T - head) / 16;
-        const uint4* v = reinterpret_cast<const uint4*>(mask + head);
-        auto bytes = [](uint32_t w) { return __popc((((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w) & 0x80808080u); };  // not 0
-        for (int64_t i = threadIdx.x; i < vecs; i += kLossThreads) {
-            const uint4 m = v[i];
-            unmasked += bytes(m.x) + bytes(m.y) + bytes(m.z) + bytes(m.w);
-        }
-        for (int64_t r = threadIdx.x; r < head; r += kLossThreads) unmasked += mask[r] != 0;
-        for (int64_t r = head + 16 * vecs + threadIdx.x; r < T; r += kLossThreads) unmasked += mask[r] != 0;
+    if (gridDim.x == 1) {
+        balance_finish(sum, live, counts, E, coef, loss, w);
+        return;
     }
-    low = wave_sum(low), high = wave_sum(high), unmasked = wave_sum(unmasked);
+    live = wave_sum(live);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
     if ((threadIdx.x & 63) == 0) {
-        uint32_t* w = tmp[threadIdx.x >> 6];
-        w[0] = low, w[1] = high, w[2] = unmasked;
+        tmp[0][threadIdx.x >> 6] = sum;
+        tmp[1][threadIdx.x >> 6] = live;
     }
     __syncthreads();
-    int64_t chosen = 0, live = 0;
+    if (threadIdx.x < 2) {
+        double s = 0;
 #pragma unroll
-    for (int w = 0; w < kLossThreads / 64; ++w) {
-        chosen += tmp[w][0] + ((int64_t)tmp[w][1] << 16);
-        live += tmp[w][2];
-    }
-    if (!mask) live = T;
-    const double unit = chosen > 0 && live > 0 ? (double)coef * E / ((double)chosen * (double)live) : 0.0;
-    float we[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = j + i * L;
-        we[i] = e < E ? (float)(unit * counts[e]) : 0.f;
-        if (blockIdx.x == 0 && (int)threadIdx.x < L && e < E) w[e] = we[i];
-    }
-    double sum = 0;
-    for (; t < T; t += step) {
-        float p[V], s = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = next[i];
-        row_load<L, V, HALF>(logits, is_live(t + step), t + step, E, next);  // while this row is reduced
-        row_softmax<L, V>(p);  // a masked row has no logits: no probabilities
-#pragma unroll
-        for (int i = 0; i < V; ++i) s = __builtin_fmaf(p[i], we[i], s);
-        sum += s;
-    }
-    sum = block_sum(sum, dtmp);
-    if (threadIdx.x == 0) {
-        if (gridDim.x == 1) *loss = (float)sum;
-        else part[blockIdx.x] = sum;
+        for (int k = 0; k < kLossThreads / 64; ++k) s += tmp[threadIdx.x][k];
+        part[2 * blockIdx.x + threadIdx.x] = s;
     }
 }
 
-__global__ __launch_bounds__(kLossThreads) void moe_balance_finish(const double* __restrict__ part, int n, float* loss) {
-    __shared__ double tmp[kLossThreads / 64];
-    double s = (int)threadIdx.x < n ? part[threadIdx.x] : 0.0;
-    s = block_sum(s, tmp);
-    if (threadIdx.x == 0) *loss = (float)s;
+__global__ __launch_bounds__(kLossThreads) void moe_balance_finish(const double* __restrict__ part, int n, int E,
+                                                                   const int32_t* __restrict__ counts, float coef, float* loss,
+                                                                   float* __restrict__ w) {
+    double sum = 0, live = 0;
+    for (int b = threadIdx.x; b < n; b += kLossThreads) {
+        sum += part[2 * b];
+        live += part[2 * b + 1];
+    }
+    balance_finish(sum, live, counts, E, coef, loss, w);
 }
 
 template <int L, int V, bool HALF>
-__global__ __launch_bounds__(kLossThreads) void moe_balance_grad_kernel(const void* __restrict__ logits, int64_t T, int E,
+__global__ __launch_bounds__(kLossThreads) void moe_balance_grad_kernel(const void* __restrict__ logits, int64_t T, int E, bool vec,
                                                                         const float* __restrict__ w,
                                                                         const uint8_t* __restrict__ mask,
                                                                         const float* __restrict__ grad, void* __restrict__ d) {
-    const int j = threadIdx.x & (L - 1);
+    const int e0 = (threadIdx.x & (L - 1)) * V;
     const float g = *grad;
     float we[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) we[i] = j + i * L < E ? w[j + i * L] : 0.f;
-    const int64_t per = kLossThreads / L, step = gridDim.x * per;
-    int64_t t = blockIdx.x * per + threadIdx.x / L;
-    auto is_live = [&](int64_t r) { return r < T && (!mask || mask[r] != 0); };
-    float next[V];
-    bool next_live = is_live(t);
-    row_load<L, V, HALF>(logits, next_live, t, E, next);
-    for (; t < T; t += step) {
-        float p[V], s = 0.f;
-        const bool live = next_live;
+    for (int i = 0; i < V; ++i) we[i] = w[min(e0 + i, E - 1)];
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = next[i];
-        next_live = is_live(t + step);
-        row_load<L, V, HALF>(logits, next_live, t + step, E, next);  // while this row is reduced
-        row_softmax<L, V>(p);
+    for (int i = 0; i < V; ++i) we[i] = e0 + i < E ? we[i] : 0.f;
+    auto row = [&](int64_t t, bool live, float (&p)[V], auto wide) __attribute__((always_inline)) {
+        float s = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) s = __builtin_fmaf(p[i], we[i], s);
         s = row_sum<L>(s);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = j + i * L;
-            if (e >= E) continue;
-            const float v = live ? g * p[i] * (we[i] - s) : 0.f;
-            if constexpr (HALF) reinterpret_cast<uint16_t*>(d)[t * E + e] = (uint16_t)bf16_rne(v);
-            else reinterpret_cast<float*>(d)[t * E + e] = v;
+        for (int i = 0; i < V; ++i) p[i] = live ? g * p[i] * (we[i] - s) : 0.f;
+        uint16_t* h = reinterpret_cast<uint16_t*>(d) + t * E + e0;
+        float* f = reinterpret_cast<float*>(d) + t * E + e0;
+        if constexpr (decltype(wide)::value) {
+            constexpr int B = V * (HALF ? 2 : 4), C = B < 16 ? B : 16;
+            uint32_t o[(B + 3) / 4];
+#pragma unroll
+            for (int i = 0; i < B / 4; ++i) {
+                if constexpr (HALF) o[i] = bf16x2_rne(p[2 * i], p[2 * i + 1]);
+                else o[i] = __float_as_uint(p[i]);
+            }
+            if (t < T && e0 < E) {
+                uint8_t* dst = HALF ? reinterpret_cast<uint8_t*>(h) : reinterpret_cast<uint8_t*>(f);
+#pragma unroll
+                for (int c = 0; c < B / C; ++c) __builtin_memcpy(__builtin_assume_aligned(dst + c * C, C), o + c * C / 4, C);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (t >= T || e0 + i >= E) continue;
+                if constexpr (HALF) h[i] = (uint16_t)bf16_rne(p[i]);
+                else f[i] = p[i];
+            }
+        }
+    };
+    if constexpr (V > 1) {
+        if (vec) {
+            for_rows<L, V, HALF, true>(logits, T, E, mask, [&](int64_t t, bool live, float (&p)[V]) __attribute__((always_inline)) {
+                row(t, live, p, std::true_type{});
+            });
+            return;
         }
     }
+    for_rows<L, V, HALF, false>(logits, T, E, mask, [&](int64_t t, bool live, float (&p)[V]) __attribute__((always_inline)) {
+        row(t, live, p, std::false_type{});
+    });
 }
 
 // calls f(L, V) for the lanes and values per lane of a row of E logits
@@ -404,10 +485,12 @@ hipError_t by_width(int64_t E, F&& f) {
     return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
 int64_t lanes_of(int64_t E) { return E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64; }
-// One workgroup, and so one launch, up to eight rounds of it; a second launch costs about as much.
+// One workgroup, and so one launch, for as many rounds as cost less than a second launch (2 us; a round after the first 0.6 us
+// for one value per lane, 0.9 for four, 2.5 for sixteen: E = 256, T = 32 4.6 us; T = 64 5.8 with a second launch, 6.4 without).
 int64_t loss_blocks(int64_t T, int64_t E) {
-    const int64_t b = (T * lanes_of(E) + kLossThreads - 1) / kLossThreads;
-    return b <= 8 ? 1 : b < kLossBlocks ? b : kLossBlocks;
+    const int64_t b = (T * lanes_of(E) + kRows * kLossThreads - 1) / (kRows * kLossThreads);
+    const int64_t values = (E + 63) / 64;
+    return b <= 1 + 24 / (6 + values) ? 1 : b < kLossBlocks ? b : kLossBlocks;
 }
 
 }  // namespace
@@ -433,7 +516,7 @@ hipError_t launch_moe_route(const void* ids, bool wide, int64_t T, int64_t top, 
 
 size_t moe_balance_workspace_bytes(int64_t T, int64_t E) {
     const int64_t b = loss_blocks(T, E);
-    return b > 1 ? (size_t)b * sizeof(double) : 0;
+    return b > 1 ? (size_t)b * 2 * sizeof(double) : 0;
 }
 
 hipError_t launch_moe_balance(const void* logits, bool half, int64_t T, int64_t E, const int32_t* counts, const uint8_t* mask,
@@ -444,26 +527,30 @@ hipError_t launch_moe_balance(const void* logits, bool half, int64_t T, int64_t 
         constexpr int L = decltype(l)::value, V = decltype(v)::value;
         const dim3 grid((unsigned)blocks), block(kLossThreads);
         if (half)
-            hipLaunchKernelGGL((moe_balance_kernel<L, V, true>), grid, block, 0, st, logits, T, (int)E, counts, mask, coef, loss, w, part);
+            hipLaunchKernelGGL((moe_balance_kernel<L, V, true>), grid, block, 0, st, logits, T, (int)E,
+                               row_vec<V, true>(logits, E), counts, mask, coef, loss, w, part);
         else
-            hipLaunchKernelGGL((moe_balance_kernel<L, V, false>), grid, block, 0, st, logits, T, (int)E, counts, mask, coef, loss, w, part);
+            hipLaunchKernelGGL((moe_balance_kernel<L, V, false>), grid, block, 0, st, logits, T, (int)E,
+                               row_vec<V, false>(logits, E), counts, mask, coef, loss, w, part);
         return hipGetLastError();
     });
     if (err != hipSuccess || blocks == 1) return err;
-    hipLaunchKernelGGL(moe_balance_finish, dim3(1), dim3(kLossThreads), 0, st, part, (int)blocks, loss);
+    hipLaunchKernelGGL(moe_balance_finish, dim3(1), dim3(kLossThreads), 0, st, part, (int)blocks, (int)E, counts, coef, loss, w);
     return hipGetLastError();
 }
 
 hipError_t launch_moe_balance_grad(const void* logits, bool half, int64_t T, int64_t E, const float* w, const uint8_t* mask,
                                    const float* grad_loss, void* dlogits, hipStream_t st) {
-    const int64_t blocks = (T * lanes_of(E) + kLossThreads - 1) / kLossThreads;
+    const int64_t blocks = (T * lanes_of(E) + kRows * kLossThreads - 1) / (kRows * kLossThreads);
     return by_width(E, [&](auto l, auto v) {
         constexpr int L = decltype(l)::value, V = decltype(v)::value;
-        const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096)), block(kLossThreads);
+        const dim3 grid((unsigned)(blocks < kLossBlocks ? blocks : kLossBlocks)), block(kLossThreads);
         if (half)
-            hipLaunchKernelGGL((moe_balance_grad_kernel<L, V, true>), grid, block, 0, st, logits, T, (int)E, w, mask, grad_loss, dlogits);
+            hipLaunchKernelGGL((moe_balance_grad_kernel<L, V, true>), grid, block, 0, st, logits, T, (int)E,
+                               row_vec<V, true>(logits, E) && row_vec<V, true>(dlogits, E), w, mask, grad_loss, dlogits);
         else
-            hipLaunchKernelGGL((moe_balance_grad_kernel<L, V, false>), grid, block, 0, st, logits, T, (int)E, w, mask, grad_loss, dlogits);
+            hipLaunchKernelGGL((moe_balance_grad_kernel<L, V, false>), grid, block, 0, st, logits, T, (int)E,
+                               row_vec<V, false>(logits, E) && row_vec<V, false>(dlogits, E), w, mask, grad_loss, dlogits);
         return hipGetLastError();
     });
 }
