@@ -367,7 +367,7 @@ mx_status moe_route(const void *ids, int id_bytes, int64_t T, int64_t top, int64
  *   loss = coef * E * sum_e f_e P_e, f_e = counts_e / sum(counts),
  *   P_e = mean over the unmasked tokens of softmax(logits[t])_e.
  *   logits [T, E] in, FP32 or BF16; counts [E] in; mask [T] bytes in or NULL: 0 marks
- *   a padded token, whose logits are not read
+ *   a padded token, whose logits count nothing, whatever they hold
  *   loss [1] FP32 out; weights [E] FP32 out: coef * E * f_e / (unmasked tokens),
  *   what moe_balance_loss_grad needs.
  * No choice or no unmasked token at all: loss and weights 0.  A row whose logits

@@ -124,6 +124,35 @@ def test_balance_loss_and_gradient(mx, t, e, half, padded):
         assert not gh[~mask].any()
 
 
+# rows that are no multiple of their loads, and rows that start between them
+@pytest.mark.parametrize("t,e,shift", [(50, 65, 0), (50, 131, 0), (3, 255, 0), (40, 257, 0), (20, 1023, 0), (40, 70, 1),
+                                       (50, 160, 1), (50, 160, 2), (40, 512, 3), (20, 1000, 1), (600, 256, 1)])
+@pytest.mark.parametrize("half", [False, True])
+def test_balance_rows_of_any_start(mx, t, e, shift, half):
+    import torch
+    rng = np.random.default_rng(t * e + shift)
+    logits = rng.normal(0, 3, (t, e))
+    mask = rng.random(t) < 0.7
+    mask[0] = True
+    logits[~mask] = np.nan
+    buf = torch.zeros(t * e + shift, dtype=torch.bfloat16 if half else torch.float32, device="cuda")
+    ld = buf[shift:].view(t, e)
+    ld.copy_(torch.from_numpy(logits))
+    logits = bf16_host(ld) if half else ld.cpu().numpy()
+    counts = rng.integers(0, 50, e).astype(np.int32)
+    coef, grad = 0.02, -1.7
+    loss, w, d, scale = _balance(logits, counts, coef, mask, np.float32(grad).astype(np.float64))
+    gl, gw = mx.moe_balance_loss(ld, to_dev(counts), coef, mask=to_dev(mask))
+    out = torch.full((t * e + shift + 8,), 7.0, dtype=ld.dtype, device="cuda")
+    mx.moe_balance_loss_grad(ld, gw, torch.tensor([grad], device="cuda"), mask=to_dev(mask), dlogits=out[shift:shift + t * e].view(t, e))
+    assert (out[:shift] == 7).all() and (out[shift + t * e:] == 7).all()
+    gd = out[shift:shift + t * e].view(t, e)
+    gh = bf16_host(gd) if half else gd.cpu().numpy().astype(np.float64)
+    assert abs(float(gl) - loss) <= (EPS + 2.0 ** -24) * loss + 1e-38
+    assert np.all(np.abs(gh - d) <= EPS * scale + (2.0 ** -8 if half else 2.0 ** -23) * np.abs(d) + 1e-38)
+    assert not gh[~mask].any()
+
+
 def test_balance_gradient_against_differences(mx):
     import torch
     rng = np.random.default_rng(1)
