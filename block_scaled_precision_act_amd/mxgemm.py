@@ -2,10 +2,11 @@
 
 Two layers:
   * the C entry points under their own names (``mx_quant_act_bf16``,
-    ``mx_gemm_a4w4_bf16``, ``ptpc_quant_act_fp8``, ``gemm_a8w8_ptpc_bf16``, ...)
+    ``mx_gemm_a4w4_bf16``, ``ptpc_quant_act_fp8``, ``gemm_a8w8_b128_bf16``,
+    ``moe_route``, ...)
     taking raw device pointers / sizes / a stream handle and returning the
     mx_status integer;
-  * tensor helpers (``quant_act_mx``, ``gemm_a4w4``, ``linear_a4w4``, ...) that
+  * tensor helpers (``quant_act_mx``, ``gemm_a4w4``, ``linear_a8w8_b128``, ...) that
     check dtypes and shapes, allocate outputs with torch and call the entry
     points on torch's current stream.
 
