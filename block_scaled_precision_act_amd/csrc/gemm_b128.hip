@@ -1,8 +1,14 @@
 // gemm_b128.hip - entries of the A8W8 GEMM with one FP32 scale per block of 128 (kernels: gemm_b128.hpp).
 //
 // Dense products take the tile whose rounds over the CUs are estimated cheapest: rounds = ceil(tiles / CUs), times the time
-// of one round of that tile (kTiles; measured at K = 8192 and N = 7168, us, launch taken off), so a small product fills the
-// CUs with small tiles and a large one is read least by large tiles.
+// of one round of that tile (kTiles; measured at K = 8192 and N = 7168, us, launch taken off, weights in the last-level
+// cache), so a small product fills the CUs with small tiles and a large one is read least by large tiles.  Over 67 shapes (M 3 to
+// 8192, N 256 to 7168, K 512 to 8192) with weights in no cache the choice takes 1% more than the best of twelve tiles, 32% at worst.
+//
+// Few rows against weights in no cache take longer than the weights' stream (N = 7168, K = 8192, M = 16 / 32 / 64 / 128: 14.0 / 17.3
+// / 19.5 / 24.9 us against 12.3 / 12.6 / 14.6 / 18.7 from the last-level cache): a CU's loads return in order, so its copies
+// of activations, from L2, queue behind those of weights.  Fetching weight lines ahead, by the copying waves or by a
+// wave of its own, takes places in the same queue and cost 2 to 4 us; tiles of 64 x 32 were as fast as 32 x 64.
 //
 // Grouped products take theirs by the same rule from the mean group (kGroupTiles; rounds at K = 7168 with weights from HBM),
 // but not below the time that the weights take from memory at 5.4 TB/s; equal ones go to the larger tile.  Groups differ
