@@ -296,7 +296,7 @@ static mx_status check_route(int64_t T, int64_t top, int64_t E) {
     const mx_status st = check_router(T, E);
     if (st != MX_SUCCESS) return st;
     if (top < 0) return MX_ERROR_INVALID_VALUE;
-    // choices are numbered in 31 bits, and the place pass reads every chunk's counts in every workgroup
+    // choices are numbered in 32 bits, and so are the counts of their chunks, with room to spare
     if (top > 0 && T > (INT64_C(1) << 24) / top) return MX_ERROR_UNSUPPORTED_SHAPE;
     return MX_SUCCESS;
 }

@@ -7,7 +7,8 @@
 //   A workgroup places a chunk of the choices and needs every expert's count, in all and in the chunks before its own.
 // Up to kAllMax choices each workgroup counts all ids itself, in LDS: one launch, no workspace.  Above, one kernel
 // counts every chunk and a second one sums the counts of the chunks (chunks * E integers, read by every workgroup)
-// before it places.  LDS atomics bound the first form (about 35 cycles for 64 random ids), a chain of memory and LDS
+// before it places.  All of them together read those in quadratic time, so from kScanMin integers on a third kernel turns them
+// into running sums in between (2^22 choices over 256 experts 55 us instead of 296, 2^24 190 us instead of 4.1 ms).  LDS atomics bound the first form (about 35 cycles for 64 random ids), a chain of memory and LDS
 // latencies the second: 512 choices over 32 experts 4.9 us, 8192 over 160 9.2 us, 24594 over 160 10.5 us (17 us in one
 // launch), 131072 over 256 10.4 us.
 //
@@ -26,6 +27,7 @@ namespace {
 constexpr int kMaxE = 1024;
 constexpr int kThreads = 512, kChunk = 2048;  // choices per workgroup
 constexpr int kAllMax = 8192;
+constexpr int64_t kScanMin = 32768;
 
 // Choices are numbered in 32 bits: T * top <= 2^24.
 __device__ __forceinline__ int id_at(const void* ids, bool wide, int i, int E) {
@@ -84,10 +86,43 @@ __global__ __launch_bounds__(kThreads) void moe_route_count(const void* ids, boo
     for (int e = threadIdx.x; e < E; e += kThreads) hist[(int64_t)blockIdx.x * E + e] = h[e];
 }
 
-// Places chunk blockIdx.x.  hist: the chunks' counts, or null: this workgroup counts all ids.  Wave w takes the w-th
+// hist[c, e] becomes the choices of expert e in the chunks before c, totals[e] those of all.  16 experts per workgroup, 32
+// threads for each, which take contiguous parts of the chunks.
+constexpr int kScanExperts = 16;
+__global__ __launch_bounds__(kThreads) void moe_route_scan(int* __restrict__ hist, int chunks, int E, int* __restrict__ totals) {
+    constexpr int PARTS = kThreads / kScanExperts;
+    __shared__ int sums[PARTS][kScanExperts];
+    const int k = threadIdx.x % kScanExperts, part = threadIdx.x / kScanExperts, e = blockIdx.x * kScanExperts + k;
+    const int per = (chunks + PARTS - 1) / PARTS, c0 = min(part * per, chunks), c1 = min(c0 + per, chunks);
+    int sum = 0;
+    if (e < E) {
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) sum += hist[(int64_t)c * E + e];
+    }
+    sums[part][k] = sum;
+    __syncthreads();
+    if (e >= E) return;
+    int before = 0;
+    for (int q = 0; q < part; ++q) before += sums[q][k];
+    if (part == PARTS - 1) totals[e] = before + sum;
+    constexpr int B = 8;  // reads ahead of the writes
+    for (int c = c0; c < c1; c += B) {
+        int v[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) v[i] = c + i < c1 ? hist[(int64_t)(c + i) * E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            if (c + i < c1) hist[(int64_t)(c + i) * E + e] = before;
+            before += v[i];
+        }
+    }
+}
+
+// Places chunk blockIdx.x.  hist: the chunks' counts (running sums if there are totals), or null: this workgroup counts all ids.  Wave w takes the w-th
 // part of the chunk in rounds of 64, its ids in registers from the start: what the kernel waits for is memory.
 __global__ __launch_bounds__(kThreads) void moe_route_place(const void* ids, bool wide, int n, int top, int E,
-                                                            const int* __restrict__ hist, int32_t* counts, int32_t* offsets,
+                                                            const int* __restrict__ hist, const int* __restrict__ totals,
+                                                            int32_t* counts, int32_t* offsets,
                                                             int32_t* rows, int32_t* slots) {
     constexpr int W = kThreads / 64, PER = kMaxE / kThreads, R = kChunk / kThreads;
     __shared__ int h[W * kMaxE], all[kMaxE], before[kMaxE];
@@ -102,7 +137,12 @@ __global__ __launch_bounds__(kThreads) void moe_route_place(const void* ids, boo
     for (int i = threadIdx.x; i < W * E; i += kThreads) h[i] = 0;
     for (int e = threadIdx.x; e < E; e += kThreads) all[e] = before[e] = 0;
     __syncthreads();
-    if (hist) {
+    if (totals) {
+        for (int e = threadIdx.x; e < E; e += kThreads) {
+            all[e] = totals[e];
+            before[e] = hist[(int64_t)chunk * E + e];
+        }
+    } else if (hist) {
         // thread t takes expert t % span of chunks t / span, t / span + parts, ...
         const int sbits = bits < 9 ? bits : 9, span = 1 << sbits, parts = kThreads >> sbits;
         static_assert(kThreads == 512, "span");
@@ -495,22 +535,30 @@ int64_t loss_blocks(int64_t T, int64_t E) {
 
 }  // namespace
 
+// the chunks' counts, then the totals
 size_t moe_route_workspace_bytes(int64_t n, int64_t E) {
-    return n <= kAllMax ? 0 : (size_t)((n + kChunk - 1) / kChunk) * E * sizeof(int);
+    return n <= kAllMax ? 0 : (size_t)((n + kChunk - 1) / kChunk + 1) * E * sizeof(int);
 }
 
 hipError_t launch_moe_route(const void* ids, bool wide, int64_t T, int64_t top, int64_t E, int32_t* counts, int32_t* offsets,
                             int32_t* rows, int32_t* slots, void* workspace, hipStream_t st) {
-    const int64_t n = T * top;
-    const dim3 grid((unsigned)(n > 0 ? (n + kChunk - 1) / kChunk : 1));
+    const int64_t n = T * top, chunks = n > 0 ? (n + kChunk - 1) / kChunk : 1;
+    const dim3 grid((unsigned)chunks);
     int* hist = n <= kAllMax ? nullptr : reinterpret_cast<int*>(workspace);
+    int* totals = hist && chunks * E >= kScanMin ? hist + chunks * E : nullptr;
     if (hist) {
         hipLaunchKernelGGL(moe_route_count, grid, dim3(kThreads), 0, st, ids, wide, (int)n, (int)E, hist);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
-    hipLaunchKernelGGL(moe_route_place, grid, dim3(kThreads), 0, st, ids, wide, (int)n, (int)top, (int)E, hist, counts, offsets, rows,
-                       slots);
+    if (totals) {
+        hipLaunchKernelGGL(moe_route_scan, dim3((unsigned)((E + kScanExperts - 1) / kScanExperts)), dim3(kThreads), 0, st, hist,
+                           (int)chunks, (int)E, totals);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    hipLaunchKernelGGL(moe_route_place, grid, dim3(kThreads), 0, st, ids, wide, (int)n, (int)top, (int)E, hist, totals, counts,
+                       offsets, rows, slots);
     return hipGetLastError();
 }
 

@@ -42,6 +42,16 @@ def test_route_exact(mx, t, top, e, wide):
         assert g.dtype == torch.int32 and np.array_equal(g.cpu().numpy(), w), name
 
 
+# from 32768 counts of chunks on: more chunks than threads for an expert, fewer, a last chunk of one, the most choices
+@pytest.mark.parametrize("t,top,e", [(70000, 8, 160), (69633, 1, 1000), (65536, 8, 129), (1 << 21, 8, 256), (1 << 24, 1, 5)])
+def test_route_many_choices(mx, t, top, e):
+    rng = np.random.default_rng(t + e)
+    ids = rng.integers(-2, e + 2, (t, top)).astype(np.int32)
+    got = mx.moe_route(to_dev(ids), e)
+    for name, g, w in zip(("counts", "offsets", "rows", "slots"), got, _route(ids, e)):
+        assert np.array_equal(g.cpu().numpy(), w), name
+
+
 @pytest.mark.parametrize("t,top,e", [(0, 4, 6), (5, 0, 6), (300, 2, 9), (9000, 2, 9)])
 def test_route_without_choices(mx, t, top, e):
     ids = np.full((t, top), -1, np.int64)
