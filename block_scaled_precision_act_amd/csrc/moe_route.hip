@@ -8,9 +8,9 @@
 // Up to kAllMax choices each workgroup counts all ids itself, in LDS: one launch, no workspace.  Above, one kernel
 // counts every chunk and a second one sums the counts of the chunks (chunks * E integers, read by every workgroup)
 // before it places.  All of them together read those in quadratic time, so from kScanMin integers on a third kernel turns them
-// into running sums in between (2^22 choices over 256 experts 55 us instead of 296, 2^24 190 us instead of 4.1 ms).  LDS atomics bound the first form (about 35 cycles for 64 random ids), a chain of memory and LDS
-// latencies the second: 512 choices over 32 experts 4.9 us, 8192 over 160 9.2 us, 24594 over 160 10.5 us (17 us in one
-// launch), 131072 over 256 10.4 us.
+// into running sums in between (2^22 choices over 256 experts 55 us instead of 296, 2^24 190 us instead of 4.1 ms).
+//   LDS atomics bound the first form (about 35 cycles for 64 random ids), a chain of memory and LDS latencies the second: 512
+// choices over 32 experts 4.9 us, 8192 over 160 9.2 us, 24594 over 160 10.5 us (17 us in one launch), 131072 over 256 10.4 us.
 //
 // Balance loss.  p = softmax(logits[t]) over the experts, f_e = counts_e / sum(counts), n the tokens whose
 // mask is not 0: loss = coef * E * sum_e f_e * mean_t p_te = sum_t sum_e w_e p_te with w_e = coef E f_e / n, so
